@@ -300,6 +300,50 @@ MOE_API int moe_ep_combine(const void* y, const int32_t* order, int n, int T, in
                            void* out, moe_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Rows by expert and back, with the gradients -- the pages compute the
+ * forward pass alone; these calls are the first and last step of a training
+ * step's expert FFN in its unfused form ([RFC] Background steps 1 and 5),
+ * around the products below.  Row buffers hold `capacity` rows (the length
+ * of sorted_token_ids) in the planner's order: row p belongs to route
+ * sorted_token_ids[p].  What is written to a row buffer covers its rows
+ * below num_tokens_post_padded: routed rows their values, padding rows
+ * zeros; rows at or past it are left as they were.
+ *
+ * moe_route_slots -- slots (T, top_k) int32, written in full: the place of
+ *   route t*top_k+j in sorted_token_ids, or -1 for a route without one (its
+ *   expert is outside [0, E)).
+ * moe_permute -- rows[slots[t][j]] = x[t].
+ * moe_permute_backward -- grad_x[t] = sum over j of grad_rows[slots[t][j]].
+ * moe_unpermute -- out[t] = sum over j of topk_weights[t][j] *
+ *   y[slots[t][j]].
+ * moe_unpermute_backward -- grad_y[slots[t][j]] = topk_weights[t][j] *
+ *   grad_out[t]; grad_weights (T, top_k) fp32 [t][j] = <grad_out[t],
+ *   y[slots[t][j]]>, 0 for a route without a slot.
+ *
+ * Token tensors are (T, K), row buffers (capacity, K), all of one call of
+ * one type (rows_dtype); any K >= 1.  Sums run in ascending j in fp32 and
+ * are rounded once; a token without slots gets zeros.  Nothing is read
+ * through a slot of -1.  A slot at or past `capacity` counts as none.
+ * Outputs must not overlap inputs.  Pointers are aligned to their element;
+ * 16-byte vectors are used where K and every pointer allow them.
+ * ---------------------------------------------------------------------- */
+enum { MOE_ROWS_BF16 = 0, MOE_ROWS_FP32 = 1 };
+
+MOE_API int moe_route_slots(const int32_t* sorted_token_ids, const int32_t* num_tokens_post_padded,
+                            int64_t capacity, int T, int top_k, int32_t* slots, moe_stream_t stream);
+MOE_API int moe_permute(const void* x, int rows_dtype, const int32_t* sorted_token_ids,
+                        const int32_t* num_tokens_post_padded, const int32_t* slots, int64_t capacity, int T,
+                        int top_k, int K, void* rows, moe_stream_t stream);
+MOE_API int moe_permute_backward(const void* grad_rows, int rows_dtype, const int32_t* slots, int64_t capacity,
+                                 int T, int top_k, int K, void* grad_x, moe_stream_t stream);
+MOE_API int moe_unpermute(const void* y, int rows_dtype, const int32_t* slots, const float* topk_weights,
+                          int64_t capacity, int T, int top_k, int K, void* out, moe_stream_t stream);
+MOE_API int moe_unpermute_backward(const void* grad_out, const void* y, int rows_dtype,
+                                   const int32_t* sorted_token_ids, const int32_t* num_tokens_post_padded,
+                                   const int32_t* slots, const float* topk_weights, int64_t capacity, int T,
+                                   int top_k, int K, void* grad_y, float* grad_weights, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * fused_moe_bf16_noalloc -- the pages have no counterpart to this call; it
  * is a convenience of this library.  It computes exactly what
  * fused_moe_bf16 computes, for callers that cannot allocate device memory

@@ -25,6 +25,10 @@ Entry points (same names as the C ABI):
 * ``moe_ep_dispatch_plan`` / ``moe_ep_dispatch_pack`` / ``moe_ep_combine`` --
   the device work around an expert-parallel exchange (DeepGEMM #411 "SM90 FP8
   x MXFP4 MegaMoE", Summary: dispatch, routed experts, combine).
+* ``moe_permute`` / ``moe_unpermute`` and their ``_backward`` -- a training
+  step's token rows in the planner's order and back (weighted sum over a
+  token's routes), with the gradients; ``moe_route_slots`` inverts the
+  planner's order for them.
 """
 from __future__ import annotations
 
@@ -41,6 +45,7 @@ __all__ = [
     "pack_scales_blocked", "pack_scales_blocked_bytes", "moe_workspace_bytes", "moe_device_status",
     "Tuning", "DTYPE_BF16", "DTYPE_MXFP8", "LIB_PATH", "fused_moe_bf16_noalloc",
     "fused_moe_bf16_noalloc_max_workspace", "moe_ep_dispatch_plan", "moe_ep_dispatch_pack", "moe_ep_combine",
+    "moe_route_slots", "moe_permute", "moe_permute_backward", "moe_unpermute", "moe_unpermute_backward",
 ]
 
 DTYPE_BF16 = 0
@@ -104,6 +109,11 @@ _SIGS = {
     "moe_ep_dispatch_pack": ([_P, _I64, _P, _I64, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P], _I),
     "moe_ep_combine": ([_P, _P, _I, _I, _I, _I, _P, _P, _P], _I),
     "fused_moe_bf16_noalloc": ([_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I64, _P, _P], _I),
+    "moe_route_slots": ([_P, _P, _I64, _I, _I, _P, _P], _I),
+    "moe_permute": ([_P, _I, _P, _P, _P, _I64, _I, _I, _I, _P, _P], _I),
+    "moe_permute_backward": ([_P, _I, _P, _I64, _I, _I, _I, _P, _P], _I),
+    "moe_unpermute": ([_P, _I, _P, _P, _I64, _I, _I, _I, _P, _P], _I),
+    "moe_unpermute_backward": ([_P, _P, _I, _P, _P, _P, _P, _I64, _I, _I, _I, _P, _P, _P], _I),
 }
 
 
@@ -537,6 +547,178 @@ def moe_ep_combine(y, order, n: int, T: int, top_k: int, out=None, slot=None, st
     with _on_device(dev, stream) as s:
         _check(load().moe_ep_combine(_ptr(y), _ptr(order), n, T, top_k, K, _ptr(slot), _ptr(out), s))
     return out
+
+
+# ---------------------------------------------------------------- training
+def _call(fn, dev, stream, *args):
+    """fn(*args, stream handle) with ``dev`` current; without a device switch when it already is."""
+    import torch
+
+    if stream is None and dev.type == "cuda" and dev.index == torch.cuda.current_device():
+        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with _on_device(dev, stream) as s:
+            rc = fn(*args, s)
+    if rc != 0:
+        _check(rc)
+
+
+def _new(shape, dtype, dev, stream):
+    """A tensor the call is about to write, allocated on the stream that will write it: memory freed by work
+    still pending on the current stream is then not handed to another one."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    elif torch.device(getattr(stream, "device", dev)) != torch.device(dev):
+        raise ValueError(f"stream belongs to {stream.device} but the tensors are on {dev}")
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _tensor(t, name, dtype, dev, shape):
+    """One argument of a training call: type, layout, device and shape (the kernels trust all four)."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != dev:
+        raise ValueError(f"all tensors must be on {dev}, got {name} on {t.device}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _rows_dtype(t, name):
+    """MOE_ROWS_* of a (rows, K) tensor."""
+    import torch
+
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {t.dim()}")
+    if t.dtype == torch.bfloat16:
+        return 0
+    if t.dtype == torch.float32:
+        return 1
+    raise TypeError(f"{name}: dtype {t.dtype} not in (torch.bfloat16, torch.float32)")
+
+
+def _slots_shape(slots):
+    import torch
+
+    if slots is None:
+        raise ValueError("slots is required")
+    if slots.dim() != 2:
+        raise ValueError("slots must be (T, top_k)")
+    T, top_k = slots.shape
+    _tensor(slots, "slots", torch.int32, slots.device, (T, top_k))
+    return T, top_k, slots.device
+
+
+def _order(sorted_token_ids, num_tokens_post_padded, dev):
+    """Capacity of the planner's order."""
+    import torch
+
+    if sorted_token_ids is None:
+        raise ValueError("sorted_token_ids is required")
+    capacity = sorted_token_ids.numel()
+    _tensor(sorted_token_ids, "sorted_token_ids", torch.int32, dev, (capacity,))
+    _tensor(num_tokens_post_padded, "num_tokens_post_padded", torch.int32, dev, (1,))
+    return capacity
+
+
+def moe_route_slots(sorted_token_ids, num_tokens_post_padded, T: int, top_k: int, slots=None, stream=None):
+    """Inverse of the planner's order: slots (T, top_k) int32, the place of every route in sorted_token_ids
+    or -1.  What moe_permute, moe_unpermute and their gradients address rows with."""
+    import torch
+
+    dev = getattr(sorted_token_ids, "device", None)
+    capacity = _order(sorted_token_ids, num_tokens_post_padded, dev)
+    if slots is None:
+        slots = _new((T, top_k), torch.int32, dev, stream)
+    _tensor(slots, "slots", torch.int32, dev, (T, top_k))
+    _call(load().moe_route_slots, dev, stream, _ptr(sorted_token_ids), _ptr(num_tokens_post_padded), capacity, T, top_k,
+          _ptr(slots))
+    return slots
+
+
+def moe_permute(x, sorted_token_ids, num_tokens_post_padded, slots, out=None, stream=None):
+    """Token rows x (T, K), bf16 or fp32, in the planner's order: returns rows (capacity, K) with
+    rows[slots[t, j]] = x[t], zeros in padding rows; rows at or past num_tokens_post_padded are not written."""
+    dt = _rows_dtype(x, "x")
+    T, top_k, dev = _slots_shape(slots)
+    K = x.shape[1]
+    _tensor(x, "x", x.dtype, dev, (T, K))
+    capacity = _order(sorted_token_ids, num_tokens_post_padded, dev)
+    if out is None:
+        out = _new((capacity, K), x.dtype, dev, stream)
+    _tensor(out, "out", x.dtype, dev, (capacity, K))
+    _call(load().moe_permute, dev, stream, _ptr(x), dt, _ptr(sorted_token_ids), _ptr(num_tokens_post_padded),
+          _ptr(slots), capacity, T, top_k, K, _ptr(out))
+    return out
+
+
+def moe_permute_backward(grad_rows, slots, out=None, stream=None):
+    """Gradient of moe_permute by x: (T, K), the sum in route order of the rows grad_rows (capacity, K) of a
+    token's routes."""
+    dt = _rows_dtype(grad_rows, "grad_rows")
+    T, top_k, dev = _slots_shape(slots)
+    capacity, K = grad_rows.shape
+    _tensor(grad_rows, "grad_rows", grad_rows.dtype, dev, (capacity, K))
+    if out is None:
+        out = _new((T, K), grad_rows.dtype, dev, stream)
+    _tensor(out, "out", grad_rows.dtype, dev, (T, K))
+    _call(load().moe_permute_backward, dev, stream, _ptr(grad_rows), dt, _ptr(slots), capacity, T, top_k, K, _ptr(out))
+    return out
+
+
+def moe_unpermute(y, slots, topk_weights, out=None, stream=None):
+    """out (T, K): per token the sum in route order of topk_weights[t, j] * y[slots[t, j]], y (capacity, K) bf16
+    or fp32; fp32 sums, one rounding."""
+    import torch
+
+    dt = _rows_dtype(y, "y")
+    T, top_k, dev = _slots_shape(slots)
+    capacity, K = y.shape
+    _tensor(y, "y", y.dtype, dev, (capacity, K))
+    _tensor(topk_weights, "topk_weights", torch.float32, dev, (T, top_k))
+    if out is None:
+        out = _new((T, K), y.dtype, dev, stream)
+    _tensor(out, "out", y.dtype, dev, (T, K))
+    _call(load().moe_unpermute, dev, stream, _ptr(y), dt, _ptr(slots), _ptr(topk_weights), capacity, T, top_k, K,
+          _ptr(out))
+    return out
+
+
+def moe_unpermute_backward(grad_out, y, sorted_token_ids, num_tokens_post_padded, slots, topk_weights, grad_y=None,
+                           grad_weights=None, stream=None):
+    """Gradients of moe_unpermute: (grad_y (capacity, K) with grad_y[slots[t, j]] = topk_weights[t, j] *
+    grad_out[t] and zeros in padding rows, grad_weights (T, top_k) fp32 = <grad_out[t], y[slots[t, j]]>)."""
+    import torch
+
+    dt = _rows_dtype(grad_out, "grad_out")
+    T, top_k, dev = _slots_shape(slots)
+    K = grad_out.shape[1]
+    _tensor(grad_out, "grad_out", grad_out.dtype, dev, (T, K))
+    capacity = _order(sorted_token_ids, num_tokens_post_padded, dev)
+    _tensor(y, "y", grad_out.dtype, dev, (capacity, K))
+    _tensor(topk_weights, "topk_weights", torch.float32, dev, (T, top_k))
+    if grad_y is None:
+        grad_y = _new((capacity, K), grad_out.dtype, dev, stream)
+    if grad_weights is None:
+        grad_weights = _new((T, top_k), torch.float32, dev, stream)
+    _tensor(grad_y, "grad_y", grad_out.dtype, dev, (capacity, K))
+    _tensor(grad_weights, "grad_weights", torch.float32, dev, (T, top_k))
+    _call(load().moe_unpermute_backward, dev, stream, _ptr(grad_out), _ptr(y), dt, _ptr(sorted_token_ids),
+          _ptr(num_tokens_post_padded), _ptr(slots), _ptr(topk_weights), capacity, T, top_k, K, _ptr(grad_y),
+          _ptr(grad_weights))
+    return grad_y, grad_weights
 
 
 def moe_device_status(stream=None, device=None):
