@@ -344,6 +344,51 @@ MOE_API int moe_unpermute_backward(const void* grad_out, const void* y, int rows
                                    int top_k, int K, void* grad_y, float* grad_weights, moe_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * The experts' products of a training step, on rows in the planner's order
+ * (moe_permute's), keeping what the gradient needs; with e the expert of row
+ * p's block and g, u the two halves of a row of h:
+ *
+ * moe_expert_up -- h = rows . w1[e]^T, act = silu(g) * u.
+ * moe_expert_down -- y = act . w2[e]^T.
+ * moe_expert_down_backward -- with ga = grad_y . w2[e] (kept in fp32) and
+ *   s = 1 / (1 + exp(-g)): grad_h = [ga u s (1 + g (1 - s)) | ga g s];
+ *   grad_w2[e] = sum over e's rows p of grad_y[p]^T act[p].
+ * moe_expert_up_backward -- grad_rows = grad_h . w1[e]; grad_w1[e] = sum over
+ *   e's rows p of grad_h[p]^T rows[p].
+ *
+ *   rows, y, grad_y, grad_rows (capacity, K), h, grad_h (capacity, N), act
+ *   (capacity, N/2), w1 (E, N, K), w2 (E, K, N/2): bf16.  Sums in fp32, one
+ *   rounding.  Row outputs are written as moe_permute writes them: routed
+ *   rows, zeros in padding rows below num_tokens_post_padded, nothing past
+ *   it.  What padding rows of the inputs hold does not matter, NaN included.
+ *   grad_w1 / grad_w2 have their weights' shape, in bf16 or fp32
+ *   (grad_dtype, MOE_ROWS_*), written in full: an expert without rows gets
+ *   zeros.  accumulate != 0 (fp32 only) adds to what is there instead.
+ *   capacity is the length of sorted_token_ids; expert_ids holds
+ *   ceil(capacity / block_m) entries, ascending over the used blocks and with
+ *   an expert's routed rows first in its last block, as moe_align writes them.
+ * Constraints: K % 8 == 0, N % 16 == 0, 1 <= E <= 1024, block_m in {16, 32,
+ * 64, 128}; row and weight buffers 16-byte aligned, outputs apart from inputs.
+ * The kernels' waits are bounded (moe_device_status).
+ * ---------------------------------------------------------------------- */
+MOE_API int moe_expert_up(const void* rows, const void* w1, const int32_t* sorted_token_ids,
+                          const int32_t* expert_ids, const int32_t* num_tokens_post_padded, int64_t capacity, int K,
+                          int N, int E, int block_m, void* h, void* act, moe_stream_t stream);
+MOE_API int moe_expert_down(const void* act, const void* w2, const int32_t* sorted_token_ids,
+                            const int32_t* expert_ids, const int32_t* num_tokens_post_padded, int64_t capacity, int K,
+                            int N, int E, int block_m, void* y, moe_stream_t stream);
+MOE_API int moe_expert_down_backward(const void* grad_y, const void* h, const void* act, const void* w2,
+                                     const int32_t* sorted_token_ids, const int32_t* expert_ids,
+                                     const int32_t* num_tokens_post_padded, int64_t capacity, int K, int N, int E,
+                                     int block_m, void* grad_h, void* grad_w2, int grad_dtype, int accumulate,
+                                     moe_stream_t stream);
+MOE_API int moe_expert_up_backward(const void* grad_h, const void* rows, const void* w1,
+                                   const int32_t* sorted_token_ids, const int32_t* expert_ids,
+                                   const int32_t* num_tokens_post_padded, int64_t capacity, int K, int N, int E,
+                                   int block_m, void* grad_rows, void* grad_w1, int grad_dtype, int accumulate,
+                                   moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * fused_moe_bf16_noalloc -- the pages have no counterpart to this call; it
  * is a convenience of this library.  It computes exactly what
  * fused_moe_bf16 computes, for callers that cannot allocate device memory

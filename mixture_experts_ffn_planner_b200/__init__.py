@@ -29,6 +29,8 @@ Entry points (same names as the C ABI):
   step's token rows in the planner's order and back (weighted sum over a
   token's routes), with the gradients; ``moe_route_slots`` inverts the
   planner's order for them.
+* ``moe_expert_up`` / ``moe_expert_down`` and their ``_backward`` -- the
+  experts' products on those rows and the gradients by rows and by weights.
 """
 from __future__ import annotations
 
@@ -46,6 +48,7 @@ __all__ = [
     "Tuning", "DTYPE_BF16", "DTYPE_MXFP8", "LIB_PATH", "fused_moe_bf16_noalloc",
     "fused_moe_bf16_noalloc_max_workspace", "moe_ep_dispatch_plan", "moe_ep_dispatch_pack", "moe_ep_combine",
     "moe_route_slots", "moe_permute", "moe_permute_backward", "moe_unpermute", "moe_unpermute_backward",
+    "moe_expert_up", "moe_expert_down", "moe_expert_down_backward", "moe_expert_up_backward",
 ]
 
 DTYPE_BF16 = 0
@@ -113,6 +116,10 @@ _SIGS = {
     "moe_permute": ([_P, _I, _P, _P, _P, _I64, _I, _I, _I, _P, _P], _I),
     "moe_permute_backward": ([_P, _I, _P, _I64, _I, _I, _I, _P, _P], _I),
     "moe_unpermute": ([_P, _I, _P, _P, _I64, _I, _I, _I, _P, _P], _I),
+    "moe_expert_up": ([_P, _P, _P, _P, _P, _I64, _I, _I, _I, _I, _P, _P, _P], _I),
+    "moe_expert_down": ([_P, _P, _P, _P, _P, _I64, _I, _I, _I, _I, _P, _P], _I),
+    "moe_expert_down_backward": ([_P, _P, _P, _P, _P, _P, _P, _I64, _I, _I, _I, _I, _P, _P, _I, _I, _P], _I),
+    "moe_expert_up_backward": ([_P, _P, _P, _P, _P, _P, _I64, _I, _I, _I, _I, _P, _P, _I, _I, _P], _I),
     "moe_unpermute_backward": ([_P, _P, _I, _P, _P, _P, _P, _I64, _I, _I, _I, _P, _P, _P], _I),
 }
 
@@ -719,6 +726,124 @@ def moe_unpermute_backward(grad_out, y, sorted_token_ids, num_tokens_post_padded
           _ptr(num_tokens_post_padded), _ptr(slots), _ptr(topk_weights), capacity, T, top_k, K, _ptr(grad_y),
           _ptr(grad_weights))
     return grad_y, grad_weights
+
+
+def _expert_plan(w, name, sorted_token_ids, expert_ids, num_tokens_post_padded, block_m):
+    """Device, capacity and the plan's pointers of an expert product, w (E, rows, cols) its weights."""
+    import torch
+
+    if w is None:
+        raise ValueError(f"{name} is required")
+    if w.dim() != 3:
+        raise ValueError(f"{name} must have three dimensions, got {w.dim()}")
+    dev = w.device
+    _tensor(w, name, torch.bfloat16, dev, tuple(w.shape))
+    capacity = _order(sorted_token_ids, num_tokens_post_padded, dev)
+    if block_m < 1:
+        raise ValueError("block_m must be positive")
+    if expert_ids is None:
+        raise ValueError("expert_ids is required")
+    blocks = (capacity + block_m - 1) // block_m
+    if expert_ids.numel() < blocks:
+        raise ValueError(f"expert_ids must hold ceil(capacity / block_m) = {blocks} entries")
+    _tensor(expert_ids, "expert_ids", torch.int32, dev, (expert_ids.numel(),))
+    return dev, capacity, (_ptr(sorted_token_ids), _ptr(expert_ids), _ptr(num_tokens_post_padded))
+
+
+def _weight_grad(grad, name, w, accumulate, dev, stream):
+    """(gradient buffer, MOE_ROWS_* of it); a new one is bf16."""
+    import torch
+
+    if grad is None:
+        if accumulate:
+            raise ValueError(f"accumulate needs {name}")
+        return _new(tuple(w.shape), torch.bfloat16, dev, stream), 0
+    if grad.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name}: dtype {grad.dtype} not in (torch.bfloat16, torch.float32)")
+    if accumulate and grad.dtype != torch.float32:
+        raise TypeError(f"{name}: accumulating needs an fp32 buffer, got {grad.dtype}")
+    _tensor(grad, name, grad.dtype, dev, tuple(w.shape))
+    return grad, int(grad.dtype == torch.float32)
+
+
+def moe_expert_up(rows, w1, sorted_token_ids, expert_ids, num_tokens_post_padded, block_m: int, h=None, act=None,
+                  stream=None):
+    """Gate/up product with SwiGLU on rows (capacity, K) in the planner's order, w1 (E, N, K), all bf16: returns
+    (h (capacity, N), act (capacity, N/2)) with h = rows . w1[e]^T and act = silu(gate) * up from the unrounded h."""
+    import torch
+
+    bf16 = torch.bfloat16
+    dev, capacity, plan = _expert_plan(w1, "w1", sorted_token_ids, expert_ids, num_tokens_post_padded, block_m)
+    E, N, K = w1.shape
+    if N % 2:
+        raise ValueError(f"N = {N} must be even (gate and up halves)")
+    _tensor(rows, "rows", bf16, dev, (capacity, K))
+    if h is None:
+        h = _new((capacity, N), bf16, dev, stream)
+    if act is None:
+        act = _new((capacity, N // 2), bf16, dev, stream)
+    _tensor(h, "h", bf16, dev, (capacity, N))
+    _tensor(act, "act", bf16, dev, (capacity, N // 2))
+    _call(load().moe_expert_up, dev, stream, _ptr(rows), _ptr(w1), *plan, capacity, K, N, E, block_m, _ptr(h), _ptr(act))
+    return h, act
+
+
+def moe_expert_down(act, w2, sorted_token_ids, expert_ids, num_tokens_post_padded, block_m: int, out=None, stream=None):
+    """Down product on act (capacity, N/2), w2 (E, K, N/2), bf16: returns y (capacity, K) = act . w2[e]^T."""
+    import torch
+
+    bf16 = torch.bfloat16
+    dev, capacity, plan = _expert_plan(w2, "w2", sorted_token_ids, expert_ids, num_tokens_post_padded, block_m)
+    E, K, half = w2.shape
+    _tensor(act, "act", bf16, dev, (capacity, half))
+    if out is None:
+        out = _new((capacity, K), bf16, dev, stream)
+    _tensor(out, "out", bf16, dev, (capacity, K))
+    _call(load().moe_expert_down, dev, stream, _ptr(act), _ptr(w2), *plan, capacity, K, 2 * half, E, block_m, _ptr(out))
+    return out
+
+
+def moe_expert_down_backward(grad_y, h, act, w2, sorted_token_ids, expert_ids, num_tokens_post_padded, block_m: int,
+                             grad_h=None, grad_w2=None, accumulate: bool = False, stream=None):
+    """Gradients of moe_expert_down and of the SwiGLU before it: grad_y (capacity, K), h (capacity, N), act
+    (capacity, N/2), w2 (E, K, N/2), bf16.  Returns (grad_h (capacity, N) bf16, grad_w2 (E, K, N/2) bf16, or fp32
+    when such a buffer is given, which accumulate=True adds to)."""
+    import torch
+
+    bf16 = torch.bfloat16
+    dev, capacity, plan = _expert_plan(w2, "w2", sorted_token_ids, expert_ids, num_tokens_post_padded, block_m)
+    E, K, half = w2.shape
+    _tensor(grad_y, "grad_y", bf16, dev, (capacity, K))
+    _tensor(h, "h", bf16, dev, (capacity, 2 * half))
+    _tensor(act, "act", bf16, dev, (capacity, half))
+    grad_w2, gdt = _weight_grad(grad_w2, "grad_w2", w2, accumulate, dev, stream)
+    if grad_h is None:
+        grad_h = _new((capacity, 2 * half), bf16, dev, stream)
+    _tensor(grad_h, "grad_h", bf16, dev, (capacity, 2 * half))
+    _call(load().moe_expert_down_backward, dev, stream, _ptr(grad_y), _ptr(h), _ptr(act), _ptr(w2), *plan, capacity, K,
+          2 * half, E, block_m, _ptr(grad_h), _ptr(grad_w2), gdt, int(accumulate))
+    return grad_h, grad_w2
+
+
+def moe_expert_up_backward(grad_h, rows, w1, sorted_token_ids, expert_ids, num_tokens_post_padded, block_m: int,
+                           grad_rows=None, grad_w1=None, accumulate: bool = False, stream=None):
+    """Gradients of the gate/up product: grad_h (capacity, N), rows (capacity, K), w1 (E, N, K), bf16.  Returns
+    (grad_rows (capacity, K) bf16, grad_w1 (E, N, K) bf16, or fp32 when such a buffer is given, which
+    accumulate=True adds to)."""
+    import torch
+
+    bf16 = torch.bfloat16
+    dev, capacity, plan = _expert_plan(w1, "w1", sorted_token_ids, expert_ids, num_tokens_post_padded, block_m)
+    E, N, K = w1.shape
+    _tensor(grad_h, "grad_h", bf16, dev, (capacity, N))
+    _tensor(rows, "rows", bf16, dev, (capacity, K))
+    grad_w1, gdt = _weight_grad(grad_w1, "grad_w1", w1, accumulate, dev, stream)
+    if grad_rows is None:
+        grad_rows = _new((capacity, K), bf16, dev, stream)
+    _tensor(grad_rows, "grad_rows", bf16, dev, (capacity, K))
+    _call(load().moe_expert_up_backward, dev, stream, _ptr(grad_h), _ptr(rows), _ptr(w1), *plan, capacity, K, N, E,
+          block_m, _ptr(grad_rows), _ptr(grad_w1), gdt, int(accumulate))
+    return grad_rows, grad_w1
 
 
 def moe_device_status(stream=None, device=None):

@@ -1204,11 +1204,7 @@ static WsLayout ws_layout(bool fp8, int T, int K, int N, int E, int top_k, int b
   return w;
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static EncodeTiledFn get_encode() {
+EncodeTiledFn tensor_map_encoder() {
   static EncodeTiledFn fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -1221,6 +1217,22 @@ static EncodeTiledFn get_encode() {
   return fn;
 }
 
+int status_word(const char* nm, int** word) {
+  static std::atomic<int*> status_ptr[kMaxDevices];  // per device; races store the same address
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cuda_fail("cudaGetDevice");
+  if (dev >= kMaxDevices) return fail(MOE_ERR_UNSUPPORTED, "%s: device index %d too large", nm, dev);
+  int* status = status_ptr[dev].load(std::memory_order_relaxed);
+  if (!status) {
+    void* sp = nullptr;
+    if (cudaGetSymbolAddress(&sp, g_moe_status) != cudaSuccess) return cuda_fail("cudaGetSymbolAddress");
+    status = static_cast<int*>(sp);
+    status_ptr[dev].store(status, std::memory_order_relaxed);
+  }
+  *word = status;
+  return MOE_OK;
+}
+
 // 2-D row-major [rows x cols] tensor, box [box_rows x 128 bytes], 128-byte swizzle.
 // Element kinds of the 2-D tensor maps: bf16, one-byte codes (e4m3 / e8m0),
 // and packed e2m1 pairs, which the copy expands into the unpacked form (each
@@ -1229,7 +1241,7 @@ static EncodeTiledFn get_encode() {
 enum TmapKind { kTmBf16, kTmU8, kTmFp4 };
 
 static int make_tmap(CUtensorMap* m, const void* base, TmapKind kind, int64_t rows, int64_t cols, int box_rows) {
-  EncodeTiledFn enc = get_encode();
+  EncodeTiledFn enc = tensor_map_encoder();
   if (!enc) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled entry point not available");
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   const int64_t row_bytes = kind == kTmBf16 ? cols * 2 : (kind == kTmU8 ? cols : cols / 2);
@@ -1395,19 +1407,9 @@ static int run_fused(const FusedArgs& a) {
   // Blocks a kernel may visit: never past the caller's sorted_token_ids /
   // expert_ids arrays, even if num_tokens_post_padded were out of range.
   const int max_blocks = static_cast<int>(std::min<int64_t>(L.cap_rows, a.capacity) / a.bm);
-  static std::atomic<int*> status_ptr[kMaxDevices];  // per device; races store the same address
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return cuda_fail("cudaGetDevice");
-  if (dev >= kMaxDevices) return fail(MOE_ERR_UNSUPPORTED, "%s: device index %d too large", nm, dev);
-  int* status = status_ptr[dev].load(std::memory_order_relaxed);
-  if (!status) {
-    void* sp = nullptr;
-    if (cudaGetSymbolAddress(&sp, g_moe_status) != cudaSuccess) return cuda_fail("cudaGetSymbolAddress");
-    status = static_cast<int*>(sp);
-    status_ptr[dev].store(status, std::memory_order_relaxed);
-  }
-
-  int rc;
+  int* status = nullptr;
+  int rc = status_word(nm, &status);
+  if (rc != MOE_OK) return rc;
   const unsigned long long wait_ns =
       a.tune && a.tune->wait_timeout_ns > 0 ? static_cast<unsigned long long>(a.tune->wait_timeout_ns) : kWaitTimeoutNs;
   const int nsm = sm_count();

@@ -83,7 +83,7 @@ struct ScatterParams {
   void* row_out;               // (capacity, K)
   float* grad_w;               // (T, top_k), or null
   int64_t capacity;
-  int T, top_k, K, tpt, pad_blocks;
+  int T, top_k, K, tpt, pad_blocks, pad_step;
 };
 
 // Blocks [0, pad_blocks) write zeros into the padding rows below the padded
@@ -94,14 +94,14 @@ __global__ void __launch_bounds__(kPermThreads) row_scatter_kernel(const Scatter
   const int nv = p.K / V::n;
   const int64_t R = static_cast<int64_t>(p.T) * p.top_k;
   if (static_cast<int>(blockIdx.x) < p.pad_blocks) {
-    // one warp looks at 32 places at a time and clears the rows of those that hold no route
+    // one warp looks at pad_step (at most 32) places at a time and clears the rows of those that hold no route
     const int lane = threadIdx.x & 31;
     const int64_t total = min(static_cast<int64_t>(max(__ldg(p.ntpp), 0)), p.capacity);
     const int64_t warps = static_cast<int64_t>(p.pad_blocks) * (kPermThreads / 32);
-    for (int64_t p0 = (static_cast<int64_t>(blockIdx.x) * (kPermThreads / 32) + (threadIdx.x >> 5)) * 32; p0 < total;
-         p0 += warps * 32) {
+    for (int64_t p0 = (static_cast<int64_t>(blockIdx.x) * (kPermThreads / 32) + (threadIdx.x >> 5)) * p.pad_step;
+         p0 < total; p0 += warps * p.pad_step) {
       bool pad = false;
-      if (p0 + lane < total) {
+      if (lane < p.pad_step && p0 + lane < total) {
         const int id = __ldg(p.sorted_ids + p0 + lane);
         pad = id < 0 || id >= R;
       }
@@ -312,8 +312,14 @@ static int run_scatter(const char* nm, ScatterParams p, int dtype, bool grad, cu
   p.tpt = threads_per_token(static_cast<int64_t>(p.K) * esize / vb);
   const int per = kPermThreads / p.tpt;
   const int64_t token_blocks = (static_cast<int64_t>(p.T) + per - 1) / per;
-  const int64_t pad_cap = static_cast<int64_t>(std::max(1, sm_count())) * 4;
-  p.pad_blocks = static_cast<int>(std::min<int64_t>((p.capacity + kPermThreads - 1) / kPermThreads, pad_cap));
+  // The padding goes over all SMs, one place a warp while they last: with 32
+  // places a warp always, a call of 8 tokens (960 padding rows of 8 KB) took
+  // 30 us on 8 blocks.
+  constexpr int kPadWarps = kPermThreads / 32;
+  const int64_t pad_warps = static_cast<int64_t>(std::max(1, sm_count())) * 4 * kPadWarps;
+  p.pad_step = static_cast<int>(std::min<int64_t>(std::max<int64_t>((p.capacity + pad_warps - 1) / pad_warps, 1), 32));
+  const int64_t pad_warps_used = std::min<int64_t>((p.capacity + p.pad_step - 1) / p.pad_step, pad_warps);
+  p.pad_blocks = static_cast<int>((pad_warps_used + kPadWarps - 1) / kPadWarps);
   const int64_t blocks = token_blocks + p.pad_blocks;
   if (blocks == 0) return MOE_OK;
   const cudaError_t err = by_access(dtype, vb, [&](auto tag, auto width) {
