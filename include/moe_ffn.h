@@ -389,6 +389,28 @@ MOE_API int moe_expert_up_backward(const void* grad_h, const void* rows, const v
                                    moe_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * moe_orthogonalize -- the experts' weight update of a training step: every
+ * matrix of a batch (E, M, N) made nearly orthogonal by Newton-Schulz steps.
+ * X = g / (|g|_F + eps), then `steps` times A = X X^T, X <- a X + (b A +
+ * c A A) X (on the transposed side for M > N, which is the same iteration).
+ *
+ *   g          (E, M, N) bf16 or fp32 (g_dtype, MOE_ROWS_*).
+ *   out        (E, M, N) bf16, overwritten; may be g itself when g is bf16.
+ *   workspace  moe_orthogonalize_workspace_bytes(E, M, N) bytes, 256-byte
+ *              aligned; needs no initialisation; calls that overlap in time
+ *              must not share it.
+ * Any E, M, N >= 1 whose tiles of 64 x 64 number fewer than 2^31, E <=
+ * 65535; steps >= 1; |a|, |b|, |c| <= 64; eps >= 0.  Matrix operands are held
+ * in fp16 with fp32 sums, the iterate in 22 bits: the iterates' entries must
+ * stay below 1023 in magnitude (the usual coefficients keep them below 2),
+ * and a matrix whose norm is below eps / 1000 loses precision.  A zero matrix
+ * gives zeros.
+ * ---------------------------------------------------------------------- */
+MOE_API int64_t moe_orthogonalize_workspace_bytes(int E, int M, int N);
+MOE_API int moe_orthogonalize(const void* g, int g_dtype, int E, int M, int N, int steps, float a, float b, float c,
+                              float eps, void* out, void* workspace, int64_t workspace_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * fused_moe_bf16_noalloc -- the pages have no counterpart to this call; it
  * is a convenience of this library.  It computes exactly what
  * fused_moe_bf16 computes, for callers that cannot allocate device memory

@@ -31,6 +31,8 @@ Entry points (same names as the C ABI):
   planner's order for them.
 * ``moe_expert_up`` / ``moe_expert_down`` and their ``_backward`` -- the
   experts' products on those rows and the gradients by rows and by weights.
+* ``moe_orthogonalize`` -- the experts' weight update made nearly orthogonal
+  by Newton-Schulz steps.
 """
 from __future__ import annotations
 
@@ -49,6 +51,7 @@ __all__ = [
     "fused_moe_bf16_noalloc_max_workspace", "moe_ep_dispatch_plan", "moe_ep_dispatch_pack", "moe_ep_combine",
     "moe_route_slots", "moe_permute", "moe_permute_backward", "moe_unpermute", "moe_unpermute_backward",
     "moe_expert_up", "moe_expert_down", "moe_expert_down_backward", "moe_expert_up_backward",
+    "moe_orthogonalize", "moe_orthogonalize_workspace_bytes",
 ]
 
 DTYPE_BF16 = 0
@@ -92,6 +95,7 @@ _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
+_F = ctypes.c_float
 
 _SIGS = {
     "moe_last_error": ([], ctypes.c_char_p),
@@ -116,6 +120,8 @@ _SIGS = {
     "moe_permute": ([_P, _I, _P, _P, _P, _I64, _I, _I, _I, _P, _P], _I),
     "moe_permute_backward": ([_P, _I, _P, _I64, _I, _I, _I, _P, _P], _I),
     "moe_unpermute": ([_P, _I, _P, _P, _I64, _I, _I, _I, _P, _P], _I),
+    "moe_orthogonalize_workspace_bytes": ([_I, _I, _I], _I64),
+    "moe_orthogonalize": ([_P, _I, _I, _I, _I, _I, _F, _F, _F, _F, _P, _P, _I64, _P], _I),
     "moe_expert_up": ([_P, _P, _P, _P, _P, _I64, _I, _I, _I, _I, _P, _P, _P], _I),
     "moe_expert_down": ([_P, _P, _P, _P, _P, _I64, _I, _I, _I, _I, _P, _P], _I),
     "moe_expert_down_backward": ([_P, _P, _P, _P, _P, _P, _P, _I64, _I, _I, _I, _I, _P, _P, _I, _I, _P], _I),
@@ -844,6 +850,42 @@ def moe_expert_up_backward(grad_h, rows, w1, sorted_token_ids, expert_ids, num_t
     _call(load().moe_expert_up_backward, dev, stream, _ptr(grad_h), _ptr(rows), _ptr(w1), *plan, capacity, K, N, E,
           block_m, _ptr(grad_rows), _ptr(grad_w1), gdt, int(accumulate))
     return grad_rows, grad_w1
+
+
+def moe_orthogonalize_workspace_bytes(E: int, M: int, N: int) -> int:
+    n = int(load().moe_orthogonalize_workspace_bytes(E, M, N))
+    if n < 0:
+        raise MoeError(-1, "moe_orthogonalize_workspace_bytes: invalid arguments")
+    return n
+
+
+def moe_orthogonalize(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), eps: float = 1e-7, out=None,
+                      workspace=None, stream=None):
+    """Every matrix of g (E, M, N), bf16 or fp32, made nearly orthogonal: X = g / (|g|_F + eps), then `steps` times
+    X <- a X + (b A + c A A) X with A = X X^T and (a, b, c) the coefficients.  Returns out (E, M, N) bf16 (which may
+    be a bf16 g itself)."""
+    import torch
+
+    if g is None:
+        raise ValueError("g is required")
+    if g.dim() != 3:
+        raise ValueError(f"g must be (E, M, N), got {g.dim()} dimensions")
+    if g.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"g: dtype {g.dtype} not in (torch.bfloat16, torch.float32)")
+    dev, shape = g.device, tuple(g.shape)
+    _tensor(g, "g", g.dtype, dev, shape)
+    a, b, c = coefficients
+    if out is None:
+        out = _new(shape, torch.bfloat16, dev, stream)
+    _tensor(out, "out", torch.bfloat16, dev, shape)
+    if g.numel() == 0:
+        return out
+    if workspace is None:
+        workspace = _new((moe_orthogonalize_workspace_bytes(*shape),), torch.uint8, dev, stream)
+    _tensor(workspace, "workspace", torch.uint8, dev, (workspace.numel(),))
+    _call(load().moe_orthogonalize, dev, stream, _ptr(g), int(g.dtype == torch.float32), *shape, steps, a, b, c, eps,
+          _ptr(out), _ptr(workspace), workspace.numel())
+    return out
 
 
 def moe_device_status(stream=None, device=None):

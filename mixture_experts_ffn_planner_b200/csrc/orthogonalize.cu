@@ -1,0 +1,547 @@
+// An expert's update made orthogonal by Newton-Schulz steps, for a batch of
+// matrices G (M x N): X = G / (|G|_F + eps), then `steps` times
+//   A = X X^T,  B = b A + c A A,  X <- a X + B X        (M <= N)
+//   A = X^T X,  B = b A + c A A,  X <- a X + X B        (M > N)
+// which is the same iteration on the shorter side; A and B are symmetric, so
+// the tall form needs no transpose either (tile_gemm.cuh reads MN-major
+// operands as they lie).
+//
+// Precision.  The matrix operands X, A and B are fp16 (11 bits; X is held
+// times kScale = 64, which keeps the entries of a unit-norm matrix of 2^22
+// elements normal), the sums fp32.  That alone is not enough on a gradient,
+// whose spectrum falls off: the step multiplies weak directions by a = 3.44,
+// and with them the rounding noise of the strong ones (error 2e-2 of the
+// result at rank S/4 + noise).  The term that carries the noise is a X, which
+// needs no matrix product, so X is kept as a pair hi + lo / 2048 (22 bits) and
+// a X is taken from the pair: 2.0e-3, of which 1.7e-3 is the rounding of the
+// bf16 result.  From the fourth step on, when X is nearly orthogonal and B
+// nearly a multiple of I, the rounding of B's diagonal is what is left; it is
+// taken out of B into fp32 and joins a: 1.9e-3 to 2.3e-3 for matrices of
+// sides 32 to 1024, Gaussian, near-low-rank or with singular values over four
+// decades.  (Earlier it must not be: B's product with the strong directions
+// has to stay in one matrix product.)
+//
+// A side of at most 64 takes another way, in 64 bits throughout: with X = Q G
+// the iteration runs on S x S matrices alone,
+//   P = a I + b A + c A A,  Q <- P Q,  A <- P A P     from A = G G^T / (|G| + eps)^2, Q = I / (|G| + eps)
+// (|G|_F^2 is the trace of G G^T), in one block a matrix, between one pass over
+// G for G G^T and one for Q G: 3 launches instead of 17, and no fp16, whose
+// noise the steps may amplify to 1e-2 on matrices of a few rows.  It takes 64
+// bits because G G^T squares G's range, and because P, Q and A commute only up
+// to rounding, which the steps amplify as well: in fp32 a 3 x 5 matrix of rank
+// one plus noise came out 6e-4 off, and 0.3 where Q stood for its transpose.
+//
+// |G|_F of a larger side is summed in 64 bits.  Every sum has a fixed order.  The launches of a call are
+// chained by programmatic dependent launch.
+#include <algorithm>
+#include <cmath>
+
+#include "tile_gemm.cuh"
+
+namespace moe {
+
+constexpr float kNsScale = 64.0f;
+constexpr int kNsDiagFrom = 3;      // steps 0, 1, 2 keep B whole
+constexpr int kNsChunks = 128;      // blocks that share a matrix's norm, at most
+constexpr int kNsThreads = 256;
+
+__device__ __forceinline__ float ns_load(const void* g, int f32, int64_t i) {
+  return f32 ? __ldg(static_cast<const float*>(g) + i)
+             : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(g) + i));
+}
+
+// 8 elements from i on; vec: a 16-byte (bf16) or two (fp32) aligned loads.
+__device__ __forceinline__ void ns_load8(const void* g, int f32, int64_t i, int n, bool vec, float (&v)[8]) {
+  if (vec) {
+    if (f32) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(g) + i));
+      const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(g) + i) + 1);
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(g) + i));
+      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = unpack_b16(w[j]);
+        v[2 * j] = f.x;
+        v[2 * j + 1] = f.y;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < n ? ns_load(g, f32, i + j) : 0.f;
+  }
+}
+
+// part[z][chunk] = sum of squares over the chunk's share of matrix z.
+__global__ void __launch_bounds__(kNsThreads)
+    ns_norm_kernel(const void* __restrict__ g, int f32, int64_t mn, int vec, double* __restrict__ part) {
+  pdl_launch_dependents();
+  const int64_t groups = (mn + 7) / 8;
+  const int64_t base = static_cast<int64_t>(blockIdx.y) * mn;
+  double sum = 0.0;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kNsThreads + threadIdx.x; i < groups;
+       i += static_cast<int64_t>(gridDim.x) * kNsThreads) {
+    float v[8];
+    ns_load8(g, f32, base + 8 * i, static_cast<int>(min(static_cast<int64_t>(8), mn - 8 * i)), vec && 8 * i + 8 <= mn, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += static_cast<double>(v[j]) * static_cast<double>(v[j]);
+  }
+  __shared__ double warps[kNsThreads / 32];
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double s = 0.0;
+    for (int w = 0; w < kNsThreads / 32; ++w) s += warps[w];
+    part[static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x] = s;
+  }
+}
+
+// hi + lo / 2048 = kNsScale * G / (|G| + eps), rows padded to ld with zeros.
+__global__ void __launch_bounds__(kNsThreads)
+    ns_init_kernel(const void* __restrict__ g, int f32, int M, int N, int ld, int vec, const double* part, int chunks,
+                   double eps, __half* __restrict__ hi, __half* __restrict__ lo) {
+  pdl_launch_dependents();
+  pdl_wait();  // the partial sums
+  double s = 0.0;
+  for (int c = 0; c < chunks; ++c) s += __ldcg(part + static_cast<int64_t>(blockIdx.y) * chunks + c);
+  const float scale = static_cast<float>(static_cast<double>(kNsScale) / (sqrt(s) + eps));
+  const int per_row = ld / 8;
+  const int64_t groups = static_cast<int64_t>(M) * per_row;
+  const int64_t z = blockIdx.y;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kNsThreads + threadIdx.x; i < groups;
+       i += static_cast<int64_t>(gridDim.x) * kNsThreads) {
+    const int64_t row = i / per_row;
+    const int col = static_cast<int>(i - row * per_row) * 8;
+    float v[8];
+    ns_load8(g, f32, (z * M + row) * N + col, N - col, vec && col + 8 <= N, v);
+    uint32_t wh[4], wl[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float x0 = v[2 * j] * scale, x1 = v[2 * j + 1] * scale;
+      wh[j] = pack_f16(x0, x1);
+      const float2 h = unpack_f16(wh[j]);
+      wl[j] = pack_f16((x0 - h.x) * kLoScale, (x1 - h.y) * kLoScale);
+    }
+    const int64_t o = (z * M + row) * ld + col;
+    *reinterpret_cast<uint4*>(hi + o) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
+    *reinterpret_cast<uint4*>(lo + o) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
+  }
+}
+
+// ------------------------------------------------------- a side of at most 64
+constexpr int kNsSmall = 64;
+constexpr int kNsSmallChunks = 32;  // blocks that share a matrix's G G^T, at most
+using NsRow64 = double[kNsSmall + 2];
+using NsRow32 = float[kNsSmall + 4];
+
+// Element (i, l) of a matrix seen from its shorter side: i < side, l < len.
+struct NsSide {
+  const void* g;
+  int f32, tall, side, len;
+  __device__ __forceinline__ int64_t at(int64_t z, int i, int l) const {
+    return z * side * len + (tall ? static_cast<int64_t>(l) * side + i : static_cast<int64_t>(i) * len + l);
+  }
+  // (i, l) of the e-th of 64 x 64 elements, consecutive in memory for consecutive e
+  __device__ __forceinline__ int i_of(int e) const { return tall ? e % kNsSmall : e / kNsSmall; }
+  __device__ __forceinline__ int l_of(int e) const { return tall ? e / kNsSmall : e % kNsSmall; }
+};
+
+__device__ __forceinline__ void ns_load4(const double* p, double (&v)[4]) {
+  const double2 a = reinterpret_cast<const double2*>(p)[0], b = reinterpret_cast<const double2*>(p)[1];
+  v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+}
+__device__ __forceinline__ void ns_load4(const float* p, double (&v)[4]) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+}
+
+// acc[r][s] += sum over k < n of x[k][i0 + r] * y[k][j0 + s]
+template <typename RowX, typename RowY>
+__device__ __forceinline__ void ns_outer(const RowX* x, const RowY* y, int n, int i0, int j0, double (&acc)[4][4]) {
+#pragma unroll 2
+  for (int k = 0; k < n; ++k) {
+    double u[4], v[4];
+    ns_load4(&x[k][i0], u);
+    ns_load4(&y[k][j0], v);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) acc[r][s] = fma(u[r], v[s], acc[r][s]);
+  }
+}
+
+// part[z][chunk] (64 x 64) = the chunk's share of G G^T.
+__global__ void __launch_bounds__(kNsThreads) ns_small_gram_kernel(const NsSide n, double* __restrict__ part) {
+  __shared__ __align__(16) NsRow32 tile[kNsSmall];  // [l][i]
+  pdl_launch_dependents();
+  const int i0 = (threadIdx.x / 16) * 4, j0 = (threadIdx.x % 16) * 4;
+  double acc[4][4] = {};
+  for (int l0 = static_cast<int>(blockIdx.x) * kNsSmall; l0 < n.len; l0 += static_cast<int>(gridDim.x) * kNsSmall) {
+    __syncthreads();
+    for (int e = threadIdx.x; e < kNsSmall * kNsSmall; e += kNsThreads) {
+      const int i = n.i_of(e), l = n.l_of(e);
+      tile[l][i] = i < n.side && l0 + l < n.len ? ns_load(n.g, n.f32, n.at(blockIdx.y, i, l0 + l)) : 0.f;
+    }
+    __syncthreads();
+    if (i0 < n.side && j0 < n.side) ns_outer(tile, tile, min(kNsSmall, n.len - l0), i0, j0, acc);
+  }
+  double* dst = part + (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kNsSmall * kNsSmall;
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int s = 0; s < 4; ++s) dst[(i0 + r) * kNsSmall + j0 + s] = acc[r][s];
+}
+
+constexpr int kNsStepsSmem = 4 * kNsSmall * static_cast<int>(sizeof(NsRow64));
+constexpr int kNsApplySmem = kNsSmall * static_cast<int>(sizeof(NsRow64) + sizeof(NsRow32));
+
+// The iteration on S x S matrices, a block a matrix; qt[z] (64 x 64) = Q^T.
+// Bound by fp64 issue: 19 products of 64^3 at 64 fmas a clock.
+__global__ void __launch_bounds__(kNsThreads)
+    ns_small_steps_kernel(const double* part, int chunks, int side, int steps, double a, double b, double c, double eps,
+                          double* __restrict__ qt) {
+  extern __shared__ __align__(16) uint8_t ns_smem[];
+  NsRow64* A = reinterpret_cast<NsRow64*>(ns_smem);
+  NsRow64 *P = A + kNsSmall, *Q = P + kNsSmall, *T = Q + kNsSmall;
+  pdl_launch_dependents();
+  pdl_wait();
+  const double* src = part + static_cast<int64_t>(blockIdx.x) * chunks * kNsSmall * kNsSmall;
+  for (int e = threadIdx.x; e < kNsSmall * kNsSmall; e += kNsThreads) {
+    double s = 0.0;
+    for (int k = 0; k < chunks; ++k) s += __ldcg(src + k * kNsSmall * kNsSmall + e);
+    A[e / kNsSmall][e % kNsSmall] = s;
+  }
+  __syncthreads();
+  double trace = 0.0;
+  for (int i = 0; i < side; ++i) trace += A[i][i];
+  const double inv = 1.0 / (sqrt(trace) + eps);
+  __syncthreads();
+  for (int e = threadIdx.x; e < kNsSmall * kNsSmall; e += kNsThreads) {
+    const int i = e / kNsSmall, j = e % kNsSmall;
+    A[i][j] = A[i][j] * inv * inv;
+    Q[i][j] = i == j && i < side ? inv : 0.0;
+  }
+  __syncthreads();
+  const int nt = (side + 3) / 4;  // 4 x 4 tiles a row
+  const bool works = static_cast<int>(threadIdx.x) < nt * nt;
+  const int i0 = works ? static_cast<int>(threadIdx.x) / nt * 4 : 0, j0 = works ? static_cast<int>(threadIdx.x) % nt * 4 : 0;
+  // dst = f(x^T y); x is A or P, which are symmetric; dst is written after all have read
+  auto product = [&](const NsRow64* x, const NsRow64* y, NsRow64* dst, auto f) {
+    double acc[4][4] = {};
+    if (works) ns_outer(x, y, side, i0, j0, acc);
+    __syncthreads();
+    if (works) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) dst[i0 + r][j0 + s] = f(i0 + r, j0 + s, acc[r][s]);
+    }
+    __syncthreads();
+  };
+  auto same = [](int, int, double v) { return v; };
+  for (int k = 0; k < steps; ++k) {
+    product(A, A, P, [&](int i, int j, double v) { return fma(c, v, fma(b, A[i][j], i == j && i < side ? a : 0.0)); });
+    product(P, Q, Q, same);
+    if (k + 1 < steps) {
+      product(P, A, T, same);
+      product(P, T, A, same);
+      // the product is symmetric only up to rounding: keep the mean
+      double m[4][4];
+      if (works) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int s = 0; s < 4; ++s) m[r][s] = 0.5 * (A[i0 + r][j0 + s] + A[j0 + s][i0 + r]);
+      }
+      __syncthreads();
+      if (works) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int s = 0; s < 4; ++s) A[i0 + r][j0 + s] = m[r][s];
+      }
+      __syncthreads();
+    }
+  }
+  double* dst = qt + static_cast<int64_t>(blockIdx.x) * kNsSmall * kNsSmall;
+  for (int e = threadIdx.x; e < kNsSmall * kNsSmall; e += kNsThreads) dst[e] = Q[e % kNsSmall][e / kNsSmall];
+}
+
+// out = Q G, 64 places of the longer side a block.
+__global__ void __launch_bounds__(kNsThreads)
+    ns_small_apply_kernel(const NsSide n, const double* qt, __nv_bfloat16* out) {
+  extern __shared__ __align__(16) uint8_t ns_smem[];
+  NsRow64* q = reinterpret_cast<NsRow64*>(ns_smem);              // [k][i]
+  NsRow32* tile = reinterpret_cast<NsRow32*>(q + kNsSmall);      // [k][l]
+  pdl_wait();
+  const int64_t z = blockIdx.y;
+  const int l0 = static_cast<int>(blockIdx.x) * kNsSmall;
+  const double* src = qt + z * kNsSmall * kNsSmall;
+  for (int e = threadIdx.x; e < kNsSmall * kNsSmall; e += kNsThreads) {
+    q[e / kNsSmall][e % kNsSmall] = __ldcg(src + e);
+    const int i = n.i_of(e), l = n.l_of(e);
+    tile[i][l] = i < n.side && l0 + l < n.len ? ns_load(n.g, n.f32, n.at(z, i, l0 + l)) : 0.f;
+  }
+  __syncthreads();
+  const int i0 = (threadIdx.x / 16) * 4, j0 = (threadIdx.x % 16) * 4;
+  double acc[4][4] = {};
+  if (i0 < n.side) ns_outer(q, tile, n.side, i0, j0, acc);
+  __syncthreads();  // this block's part of g has been read: out may be g
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int s = 0; s < 4; ++s) tile[i0 + r][j0 + s] = static_cast<float>(acc[r][s]);
+  __syncthreads();
+  for (int e = threadIdx.x; e < kNsSmall * kNsSmall; e += kNsThreads) {
+    const int i = n.i_of(e), l = n.l_of(e);
+    if (i < n.side && l0 + l < n.len) out[n.at(z, i, l0 + l)] = __float2bfloat16_rn(tile[i][l]);
+  }
+}
+
+static int ns_small_chunks(int M, int N) { return std::min((std::max(M, N) + kNsSmall - 1) / kNsSmall, kNsSmallChunks); }
+
+static int run_ns_small(const char* nm, const void* g, int f32, int E, int M, int N, int steps, float a, float b,
+                        float c, float eps, void* out, uint8_t* ws, cudaStream_t stream) {
+  const NsSide n{g, f32, M > N ? 1 : 0, std::min(M, N), std::max(M, N)};
+  const int chunks = ns_small_chunks(M, N);
+  double* qt = reinterpret_cast<double*>(ws);
+  double* part = qt + static_cast<int64_t>(E) * kNsSmall * kNsSmall;
+  cudaError_t err = cudaFuncSetAttribute(ns_small_steps_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsStepsSmem);
+  if (err == cudaSuccess)
+    err = cudaFuncSetAttribute(ns_small_apply_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsApplySmem);
+  if (err != cudaSuccess) return cuda_fail(nm, err);
+  ns_small_gram_kernel<<<dim3(chunks, E), kNsThreads, 0, stream>>>(n, part);
+  err = cudaGetLastError();
+  if (err != cudaSuccess) return cuda_fail(nm, err);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(E, 1, 1);
+  cfg.blockDim = dim3(kNsThreads, 1, 1);
+  cfg.dynamicSmemBytes = kNsStepsSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  err = cudaLaunchKernelEx(&cfg, ns_small_steps_kernel, static_cast<const double*>(part), chunks, n.side, steps,
+                           static_cast<double>(a), static_cast<double>(b), static_cast<double>(c),
+                           static_cast<double>(eps), qt);
+  if (err != cudaSuccess) return cuda_fail(nm, err);
+  cfg.gridDim = dim3((n.len + kNsSmall - 1) / kNsSmall, E, 1);
+  cfg.dynamicSmemBytes = kNsApplySmem;
+  err = cudaLaunchKernelEx(&cfg, ns_small_apply_kernel, n, static_cast<const double*>(qt),
+                           static_cast<__nv_bfloat16*>(out));
+  return err == cudaSuccess ? MOE_OK : cuda_fail(nm, err);
+}
+
+// ------------------------------------------------------------- larger sides
+struct NsLayout {
+  int64_t hi[2], lo[2], gram, poly, diag, part, total;
+  int ldx, lds, side, chunks;
+};
+
+static NsLayout ns_layout(int E, int M, int N) {
+  NsLayout L{};
+  if (std::min(M, N) <= kNsSmall) {
+    L.total = static_cast<int64_t>(E) * (1 + ns_small_chunks(M, N)) * kNsSmall * kNsSmall * 8;
+    return L;
+  }
+  auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b * b; };
+  L.side = std::min(M, N);
+  L.ldx = static_cast<int>(up(N, 8));
+  L.lds = static_cast<int>(up(L.side, 8));
+  L.chunks = static_cast<int>(std::min<int64_t>((static_cast<int64_t>(M) * N + 8 * kNsThreads - 1) / (8 * kNsThreads), kNsChunks));
+  const int64_t x = up(static_cast<int64_t>(E) * M * L.ldx * 2, 256), s = up(static_cast<int64_t>(E) * L.side * L.lds * 2, 256);
+  int64_t off = 0;
+  auto take = [&](int64_t n) {
+    const int64_t o = off;
+    off += up(n, 256);
+    return o;
+  };
+  for (int i = 0; i < 2; ++i) {
+    L.hi[i] = take(x);
+    L.lo[i] = take(x);
+  }
+  L.gram = take(s);
+  L.poly = take(s);
+  L.diag = take(static_cast<int64_t>(E) * L.side * 4);
+  L.part = take(static_cast<int64_t>(E) * L.chunks * 8);
+  L.total = off;
+  return L;
+}
+
+struct NsCall {
+  const char* nm;
+  int E, M, N, steps;
+  float a, b, c;
+  uint8_t* ws;
+  NsLayout L;
+  void* out;
+  bool direct;  // the result cannot go through a tensor map: rows not a multiple of 16 bytes
+  cudaStream_t stream;
+};
+
+template <bool kTall, int TN>
+static int ns_steps(const NsCall& n) {
+  const NsLayout& L = n.L;
+  const int S = L.side;
+  auto xmap = [&](CUtensorMap* m, int64_t off, int b0, int b1) {
+    return make_map3(m, n.ws + off, Elem::F16, n.N, n.M, n.E, int64_t(L.ldx) * 2, int64_t(n.M) * L.ldx * 2, b0, b1, 1);
+  };
+  auto smap = [&](CUtensorMap* m, int64_t off, int b0, int b1) {
+    return make_map3(m, n.ws + off, Elem::F16, S, S, n.E, int64_t(L.lds) * 2, int64_t(S) * L.lds * 2, b0, b1, 1);
+  };
+  // operands of the three products and the store form of every buffer
+  CUtensorMap xa[2], xb[2], xs_hi[2], xs_lo[2], xk[2], gram_a, gram_b, gram_s, poly_a, poly_b, poly_s, out_s;
+  int rc = MOE_OK;
+  for (int i = 0; i < 2 && rc == MOE_OK; ++i) {
+    if (kTall) {
+      rc = xmap(&xa[i], L.hi[i], 64, kGK);                          // X^T X: both MN-major
+      if (rc == MOE_OK) rc = xmap(&xk[i], L.hi[i], kGK, kGM);       // X B: K-major
+      xb[i] = xa[i];
+    } else {
+      rc = xmap(&xa[i], L.hi[i], kGK, kGM);                         // X X^T: both K-major
+      if (rc == MOE_OK) rc = xmap(&xb[i], L.hi[i], kGK, TN);
+      if (rc == MOE_OK) rc = xmap(&xk[i], L.hi[i], 64, kGK);        // B X: MN-major
+    }
+    if (rc == MOE_OK) rc = xmap(&xs_hi[i], L.hi[i], 32, 32);
+    if (rc == MOE_OK) rc = xmap(&xs_lo[i], L.lo[i], 32, 32);
+  }
+  if (rc == MOE_OK) rc = smap(&gram_a, L.gram, kGK, kGM);
+  if (rc == MOE_OK) rc = smap(&gram_b, L.gram, kGK, TN);
+  if (rc == MOE_OK) rc = smap(&gram_s, L.gram, 64, 32);
+  if (rc == MOE_OK) rc = smap(&poly_a, L.poly, kGK, kGM);
+  if (rc == MOE_OK) rc = smap(&poly_b, L.poly, kGK, TN);
+  if (rc == MOE_OK) rc = smap(&poly_s, L.poly, 64, 32);
+  out_s = xs_hi[0];
+  if (rc == MOE_OK && !n.direct)
+    rc = make_map3(&out_s, n.out, Elem::Bf16, n.N, n.M, n.E, int64_t(n.N) * 2, int64_t(n.M) * n.N * 2, 32, 32, 1);
+  if (rc != MOE_OK) return rc;
+
+  GemmParams base{};
+  if ((rc = status_word(n.nm, &base.status)) != MOE_OK) return rc;
+  base.wait_ns = kWaitTimeoutNs;
+  base.batches = n.E;
+  base.a_rows = kGM;
+  base.store_rows = 32;
+  base.side = S;
+  base.diag = reinterpret_cast<float*>(n.ws + L.diag);
+  base.tall = kTall ? 1 : 0;
+  auto tiles = [&](GemmParams* p, int m, int cols, int k) {
+    p->m_total = m;
+    p->n_total = cols;
+    p->m_tiles = (m + kGM - 1) / kGM;
+    p->n_tiles = (cols + TN - 1) / TN;
+    p->nk = (k + kGK - 1) / kGK;
+    return static_cast<int64_t>(n.E) * p->m_tiles * p->n_tiles;
+  };
+  for (int i = 0; i < n.steps; ++i) {
+    const int cur = i & 1, nxt = cur ^ 1;
+    GemmParams p = base;
+    int64_t units = tiles(&p, S, S, kTall ? n.M : n.N);
+    p.alpha = 1.0f / (kNsScale * kNsScale);
+    rc = launch_tile_gemm<kTall ? Form::TN : Form::NT, Sched::Batch, Epi::Gram, TN, false>(
+        n.nm, xa[cur], xb[cur], gram_s, gram_s, p, units, true, n.stream);
+    if (rc != MOE_OK) return rc;
+    p = base;
+    units = tiles(&p, S, S, S);
+    p.alpha = n.c;
+    p.beta = n.b;
+    p.use_diag = i >= kNsDiagFrom ? 1 : 0;
+    p.c0 = reinterpret_cast<const __half*>(n.ws + L.gram);
+    p.ldc = L.lds;
+    p.zc = int64_t(S) * L.lds;
+    rc = launch_tile_gemm<Form::NT, Sched::Batch, Epi::Poly, TN, false>(n.nm, gram_a, gram_b, poly_s, poly_s, p, units,
+                                                                       true, n.stream);
+    if (rc != MOE_OK) return rc;
+    p = base;
+    units = tiles(&p, n.M, n.N, S);
+    p.alpha = n.a;
+    p.beta = 1.0f / kNsScale;
+    p.use_diag = i >= kNsDiagFrom ? 1 : 0;
+    p.c0 = reinterpret_cast<const __half*>(n.ws + L.hi[cur]);
+    p.c1 = reinterpret_cast<const __half*>(n.ws + L.lo[cur]);
+    p.ldc = L.ldx;
+    p.zc = int64_t(n.M) * L.ldx;
+    p.last = i + 1 == n.steps ? 1 : 0;
+    p.direct = n.direct ? 1 : 0;
+    p.out = static_cast<__nv_bfloat16*>(n.out);
+    rc = kTall ? launch_tile_gemm<Form::NT, Sched::Batch, Epi::Update, TN, false>(
+                     n.nm, xk[cur], poly_b, p.last ? out_s : xs_hi[nxt], xs_lo[nxt], p, units, true, n.stream)
+               : launch_tile_gemm<Form::NN, Sched::Batch, Epi::Update, TN, false>(
+                     n.nm, poly_a, xk[cur], p.last ? out_s : xs_hi[nxt], xs_lo[nxt], p, units, true, n.stream);
+    if (rc != MOE_OK) return rc;
+  }
+  return MOE_OK;
+}
+
+static bool ns_sizes_ok(int E, int M, int N) {
+  if (E < 1 || M < 1 || N < 1) return false;
+  const int64_t tiles = ((int64_t(M) + 63) / 64) * ((int64_t(N) + 63) / 64);
+  return E <= 65535 && tiles * E < (int64_t(1) << 31) && int64_t(M) * N < (int64_t(1) << 40);
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int64_t moe_orthogonalize_workspace_bytes(int E, int M, int N) {
+  return ns_sizes_ok(E, M, N) ? ns_layout(E, M, N).total : -1;
+}
+
+extern "C" int moe_orthogonalize(const void* g, int g_dtype, int E, int M, int N, int steps, float a, float b, float c,
+                                 float eps, void* out, void* workspace, int64_t workspace_bytes,
+                                 moe_stream_t stream) {
+  const char* nm = "moe_orthogonalize";
+  if (E < 0 || M < 0 || N < 0 || steps < 1)
+    return fail(MOE_ERR_INVALID_ARG, "%s: need E, M, N >= 0 and steps >= 1", nm);
+  if (g_dtype != MOE_ROWS_BF16 && g_dtype != MOE_ROWS_FP32) return fail(MOE_ERR_UNSUPPORTED, "%s: g must be bf16 or fp32", nm);
+  if (!(eps >= 0.0f)) return fail(MOE_ERR_INVALID_ARG, "%s: eps must be >= 0", nm);
+  if (!(std::abs(a) <= 64.0f && std::abs(b) <= 64.0f && std::abs(c) <= 64.0f))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: coefficients must be within [-64, 64]", nm);
+  if (E == 0 || M == 0 || N == 0) return MOE_OK;
+  if (!ns_sizes_ok(E, M, N)) return fail(MOE_ERR_UNSUPPORTED, "%s: too many tiles", nm);
+  if (!g || !out || !workspace) return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", nm);
+  const int esize = g_dtype == MOE_ROWS_FP32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(g) % esize || reinterpret_cast<uintptr_t>(out) % 2 ||
+      reinterpret_cast<uintptr_t>(workspace) % 256)
+    return fail(MOE_ERR_ALIGNMENT, "%s: g and out aligned to their element, the workspace to 256 bytes", nm);
+  NsCall n{nm, E, M, N, steps, a, b, c, static_cast<uint8_t*>(workspace), ns_layout(E, M, N), out, false,
+           reinterpret_cast<cudaStream_t>(stream)};
+  if (workspace_bytes < n.L.total)
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace %lld bytes < required %lld", nm, (long long)workspace_bytes,
+                (long long)n.L.total);
+  n.direct = N % 8 != 0 || reinterpret_cast<uintptr_t>(out) % 16 != 0;
+
+  const int64_t mn = int64_t(M) * N;
+  const int f32 = g_dtype == MOE_ROWS_FP32 ? 1 : 0;
+  if (std::min(M, N) <= kNsSmall) return run_ns_small(nm, g, f32, E, M, N, steps, a, b, c, eps, out, n.ws, n.stream);
+  const bool al = reinterpret_cast<uintptr_t>(g) % 16 == 0;
+  double* part = reinterpret_cast<double*>(n.ws + n.L.part);
+  ns_norm_kernel<<<dim3(n.L.chunks, E), kNsThreads, 0, n.stream>>>(g, f32, mn, al && mn % 8 == 0 ? 1 : 0, part);
+  cudaError_t err = cudaGetLastError();
+  if (err != cudaSuccess) return cuda_fail(nm, err);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  const int64_t groups = int64_t(M) * (n.L.ldx / 8);
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>((groups + kNsThreads - 1) / kNsThreads, 1024)), E, 1);
+  cfg.blockDim = dim3(kNsThreads, 1, 1);
+  cfg.stream = n.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  err = cudaLaunchKernelEx(&cfg, ns_init_kernel, g, f32, M, N, n.L.ldx, al && N % 8 == 0 ? 1 : 0,
+                           static_cast<const double*>(part), n.L.chunks, static_cast<double>(eps),
+                           reinterpret_cast<__half*>(n.ws + n.L.hi[0]), reinterpret_cast<__half*>(n.ws + n.L.lo[0]));
+  if (err != cudaSuccess) return cuda_fail(nm, err);
+  // 256-column tiles where they fill the SMs, else 128 for twice as many
+  const int64_t t256 = int64_t(E) * ((M + kGM - 1) / kGM) * ((N + 255) / 256);
+  const bool wide_tiles = t256 >= sm_count();
+  if (M > N) return wide_tiles ? ns_steps<true, 256>(n) : ns_steps<true, 128>(n);
+  return wide_tiles ? ns_steps<false, 256>(n) : ns_steps<false, 128>(n);
+}
