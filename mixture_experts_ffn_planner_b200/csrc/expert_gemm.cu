@@ -15,6 +15,14 @@
 
 namespace moe {
 
+// Pairs of CTAs take tiles of 256 x 256, single ones 128 x 128, with twice the
+// bytes from L2 a flop but four times as many tiles.  Single against pair, us,
+// at K = N = 2048 on 64 experts: up 218 and 172 at 256 rows an expert, 676 and
+// 469 at 1024, 27 and 31 at 16; at K = 4096, N = 512 on 8 experts, where pairs
+// have 16 tiles, 35 and 39 at 256 rows.
+constexpr int64_t kPairRows = 192;   // rows an expert from which a 256-row tile is filled well enough
+constexpr int64_t kPairTiles = 37;   // tiles that keep half of the pairs busy
+
 struct ExpertCall {
   const char* nm;
   const int32_t* sorted_ids;
@@ -87,71 +95,88 @@ static int weights_map(CUtensorMap* m, const void* base, Elem el, int64_t cols, 
   return make_map3(m, base, el, cols, rows, n, cols * es, cols * rows * es, b0, b1, 1);
 }
 
+// Routed rows an expert has on average, at most: the planner's capacity is
+// routes + E (block_m - 1).
+static int64_t mean_rows(const ExpertCall& c) {
+  return std::max<int64_t>(0, c.capacity - static_cast<int64_t>(c.E) * (c.bm - 1)) / c.E;
+}
+
 // rows of `width_in` times the expert's weights, into rows of width_out.
-template <Form kForm, Epi kEpi, int TN>
-static int run_blocks(const ExpertCall& c, const void* in, int64_t width_in, const void* w, int64_t w_cols,
-                      int64_t w_rows, int64_t width_out, void* out, void* out2, const void* h) {
-  if (c.capacity / c.bm == 0) return MOE_OK;
+template <Form kForm, Epi kEpi, bool kPair>
+static int blocks_tiled(const ExpertCall& c, const void* in, int64_t width_in, const void* w, int64_t w_cols,
+                        int64_t w_rows, int64_t width_out, void* out, void* out2, const void* h) {
   GemmParams p;
   if (int rc = base_params(c, &p)) return rc;
-  constexpr int kCols = kEpi == Epi::GateUp ? TN / 2 : TN;
+  constexpr int kCols = kEpi == Epi::GateUp ? tile_n(kPair) / 2 : tile_n(kPair);
   p.n_total = static_cast<int>(width_out);
   p.n_tiles = static_cast<int>(ceil_div(width_out, kCols));
   p.nk = static_cast<int>(ceil_div(width_in, kGK));
-  p.a_rows = c.bm;
   p.store_rows = std::min(c.bm, 32);
-  p.h = static_cast<const __nv_bfloat16*>(h);
-  CUtensorMap ma, mb, md, md2;
-  int rc = rows_map(&ma, c, in, width_in, kGK, c.bm);
+  GemmMaps m;
+  int rc = rows_map(&m.a, c, in, width_in, kGK, 128);
   if (rc == MOE_OK) {
     if (kForm == Form::NN)
-      rc = weights_map(&mb, w, Elem::Bf16, w_cols, w_rows, c.E, 64, kGK);
+      rc = weights_map(&m.b, w, Elem::Bf16, w_cols, w_rows, c.E, 64, kGK);
     else if (kEpi == Epi::GateUp)
-      rc = weights_map(&mb, w, Elem::Bf16, w_cols, w_rows / 2, 2 * static_cast<int64_t>(c.E), kGK, TN / 2);
+      rc = weights_map(&m.b, w, Elem::Bf16, w_cols, w_rows / 2, 2 * static_cast<int64_t>(c.E), kGK, kPair ? 128 : 64);
     else
-      rc = weights_map(&mb, w, Elem::Bf16, w_cols, w_rows, c.E, kGK, TN);
+      rc = weights_map(&m.b, w, Elem::Bf16, w_cols, w_rows, c.E, kGK, 128);
   }
   if (rc == MOE_OK) {
-    if (kEpi == Epi::GateUp) {
-      rc = halves_map(&md, c, out, width_out, 64, p.store_rows);
-      if (rc == MOE_OK) rc = rows_map(&md2, c, out2, width_out, 64, p.store_rows);
-    } else if (kEpi == Epi::SwigluGrad) {
-      rc = halves_map(&md, c, out, width_out, 32, p.store_rows);
-      md2 = md;
-    } else {
-      rc = rows_map(&md, c, out, width_out, 64, p.store_rows);
-      md2 = md;
-    }
+    if (kEpi == Epi::Rows)
+      rc = rows_map(&m.d, c, out, width_out, 64, p.store_rows);
+    else
+      rc = halves_map(&m.d, c, out, width_out, 32, p.store_rows);
   }
+  m.d2 = m.c = m.c2 = m.d;
+  if (rc == MOE_OK && kEpi == Epi::GateUp) rc = rows_map(&m.d2, c, out2, width_out, 32, p.store_rows);
+  if (rc == MOE_OK && kEpi == Epi::SwigluGrad) rc = halves_map(&m.c, c, h, width_out, 32, p.store_rows);
   if (rc != MOE_OK) return rc;
-  return launch_tile_gemm<kForm, Sched::Blocks, kEpi, TN, true>(
-      c.nm, ma, mb, md, md2, p, static_cast<int64_t>(p.max_blocks) * p.n_tiles, false, c.stream);
+  return launch_tile_gemm<kForm, Sched::Blocks, kEpi, kPair, true>(
+      c.nm, m, p, static_cast<int64_t>(p.max_blocks) * p.n_tiles, false, c.stream);
+}
+
+// cols: columns of the product.
+template <Form kForm, Epi kEpi, typename... Args>
+static int run_blocks(const ExpertCall& c, int64_t cols, Args... args) {
+  if (c.capacity / c.bm == 0) return MOE_OK;
+  const int64_t rows = mean_rows(c);
+  return rows >= kPairRows && c.E * ceil_div(rows, 256) * ceil_div(cols, 256) >= kPairTiles
+             ? blocks_tiled<kForm, kEpi, true>(c, args...)
+             : blocks_tiled<kForm, kEpi, false>(c, args...);
 }
 
 // grad[e] (m x n) = sum over e's rows of a^T b, a (capacity, m), b (capacity, n).
-template <int TN>
-static int run_weights(const ExpertCall& c, const void* a, int64_t m, const void* b, int64_t n, void* grad, int f32,
-                       int accumulate) {
+template <bool kPair>
+static int weights_tiled(const ExpertCall& c, const void* a, int64_t m, const void* b, int64_t n, void* grad, int f32,
+                         int accumulate) {
   GemmParams p;
   if (int rc = base_params(c, &p)) return rc;
   p.batches = c.E;
   p.m_total = static_cast<int>(m);
   p.n_total = static_cast<int>(n);
-  p.m_tiles = static_cast<int>(ceil_div(m, kGM));
-  p.n_tiles = static_cast<int>(ceil_div(n, TN));
+  p.m_tiles = static_cast<int>(ceil_div(m, tile_m(kPair)));
+  p.n_tiles = static_cast<int>(ceil_div(n, tile_n(kPair)));
   p.store_rows = 32;
   p.out_f32 = f32;
   p.accumulate = accumulate;
-  CUtensorMap ma, mb, md;
+  GemmMaps t;
   ExpertCall one = c;  // a tensor map needs at least one row; without capacity no row is read
   one.capacity = std::max<int64_t>(c.capacity, 1);
-  const void* dummy = grad;
-  int rc = rows_map(&ma, one, c.capacity ? a : dummy, m, 64, kGK);
-  if (rc == MOE_OK) rc = rows_map(&mb, one, c.capacity ? b : dummy, n, 64, kGK);
-  if (rc == MOE_OK) rc = weights_map(&md, grad, f32 ? Elem::F32 : Elem::Bf16, n, m, c.E, f32 ? 32 : 64, 32);
+  int rc = rows_map(&t.a, one, c.capacity ? a : grad, m, 64, kGK);
+  if (rc == MOE_OK) rc = rows_map(&t.b, one, c.capacity ? b : grad, n, 64, kGK);
+  if (rc == MOE_OK) rc = weights_map(&t.d, grad, f32 ? Elem::F32 : Elem::Bf16, n, m, c.E, f32 ? 32 : 64, 32);
   if (rc != MOE_OK) return rc;
-  return launch_tile_gemm<Form::TN, Sched::Experts, Epi::Weights, TN, true>(
-      c.nm, ma, mb, md, md, p, static_cast<int64_t>(c.E) * p.m_tiles * p.n_tiles, false, c.stream);
+  t.d2 = t.c = t.c2 = t.d;
+  return launch_tile_gemm<Form::TN, Sched::Experts, Epi::Weights, kPair, true>(
+      c.nm, t, p, static_cast<int64_t>(c.E) * p.m_tiles * p.n_tiles, false, c.stream);
+}
+
+static int run_weights(const ExpertCall& c, const void* a, int64_t m, const void* b, int64_t n, void* grad, int f32,
+                       int accumulate) {
+  return c.E * ceil_div(m, 256) * ceil_div(n, 256) >= kPairTiles
+             ? weights_tiled<true>(c, a, m, b, n, grad, f32, accumulate)
+             : weights_tiled<false>(c, a, m, b, n, grad, f32, accumulate);
 }
 
 static int check_grad(const ExpertCall& c, int dtype, int accumulate) {
@@ -172,7 +197,7 @@ extern "C" int moe_expert_up(const void* rows, const void* w1, const int32_t* so
   const ExpertCall c{"moe_expert_up", sorted_token_ids, expert_ids, num_tokens_post_padded, capacity, K, N, E, block_m,
                      reinterpret_cast<cudaStream_t>(stream)};
   if (int rc = check_expert(c, {rows, h, act}, {w1})) return rc;
-  return run_blocks<Form::NT, Epi::GateUp, 256>(c, rows, K, w1, K, N, N / 2, h, act, nullptr);
+  return run_blocks<Form::NT, Epi::GateUp>(c, N, rows, K, w1, K, N, N / 2, h, act, nullptr);
 }
 
 extern "C" int moe_expert_down(const void* act, const void* w2, const int32_t* sorted_token_ids,
@@ -181,7 +206,7 @@ extern "C" int moe_expert_down(const void* act, const void* w2, const int32_t* s
   const ExpertCall c{"moe_expert_down", sorted_token_ids, expert_ids, num_tokens_post_padded, capacity, K, N, E,
                      block_m, reinterpret_cast<cudaStream_t>(stream)};
   if (int rc = check_expert(c, {act, y}, {w2})) return rc;
-  return run_blocks<Form::NT, Epi::Rows, 256>(c, act, N / 2, w2, N / 2, K, K, y, nullptr, nullptr);
+  return run_blocks<Form::NT, Epi::Rows>(c, K, act, N / 2, w2, N / 2, K, K, y, nullptr, nullptr);
 }
 
 extern "C" int moe_expert_down_backward(const void* grad_y, const void* h, const void* act, const void* w2,
@@ -193,9 +218,9 @@ extern "C" int moe_expert_down_backward(const void* grad_y, const void* h, const
                      E, block_m, reinterpret_cast<cudaStream_t>(stream)};
   if (int rc = check_grad(c, grad_dtype, accumulate)) return rc;
   if (int rc = check_expert(c, {grad_y, h, act, grad_h}, {w2, grad_w2})) return rc;
-  if (int rc = run_blocks<Form::NN, Epi::SwigluGrad, 256>(c, grad_y, K, w2, N / 2, K, N / 2, grad_h, nullptr, h))
+  if (int rc = run_blocks<Form::NN, Epi::SwigluGrad>(c, N / 2, grad_y, K, w2, N / 2, K, N / 2, grad_h, nullptr, h))
     return rc;
-  return run_weights<256>(c, grad_y, K, act, N / 2, grad_w2, grad_dtype == MOE_ROWS_FP32, accumulate);
+  return run_weights(c, grad_y, K, act, N / 2, grad_w2, grad_dtype == MOE_ROWS_FP32, accumulate);
 }
 
 extern "C" int moe_expert_up_backward(const void* grad_h, const void* rows, const void* w1,
@@ -207,6 +232,6 @@ extern "C" int moe_expert_up_backward(const void* grad_h, const void* rows, cons
                      block_m, reinterpret_cast<cudaStream_t>(stream)};
   if (int rc = check_grad(c, grad_dtype, accumulate)) return rc;
   if (int rc = check_expert(c, {grad_h, rows, grad_rows}, {w1, grad_w1})) return rc;
-  if (int rc = run_blocks<Form::NN, Epi::Rows, 256>(c, grad_h, N, w1, K, N, K, grad_rows, nullptr, nullptr)) return rc;
-  return run_weights<256>(c, grad_h, N, rows, K, grad_w1, grad_dtype == MOE_ROWS_FP32, accumulate);
+  if (int rc = run_blocks<Form::NN, Epi::Rows>(c, K, grad_h, N, w1, K, N, K, grad_rows, nullptr, nullptr)) return rc;
+  return run_weights(c, grad_h, N, rows, K, grad_w1, grad_dtype == MOE_ROWS_FP32, accumulate);
 }

@@ -53,19 +53,6 @@ __host__ __device__ inline size_t align_smem_base(int E) {
   return sizeof(int32_t) * (static_cast<size_t>(kAlignWarps) * E + 3 * static_cast<size_t>(E) + 1 + kAlignWarps);
 }
 
-__device__ __forceinline__ uint32_t cluster_ctarank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_nctarank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // Reads a 32-bit word of CTA `rank`'s shared memory at the address that
 // `local` has in this CTA.
 __device__ __forceinline__ int32_t ld_dsmem(const int32_t* local, uint32_t rank) {

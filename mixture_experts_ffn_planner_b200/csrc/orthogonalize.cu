@@ -106,9 +106,17 @@ __global__ void __launch_bounds__(kNsThreads)
                    double eps, __half* __restrict__ hi, __half* __restrict__ lo) {
   pdl_launch_dependents();
   pdl_wait();  // the partial sums
-  double s = 0.0;
-  for (int c = 0; c < chunks; ++c) s += __ldcg(part + static_cast<int64_t>(blockIdx.y) * chunks + c);
-  const float scale = static_cast<float>(static_cast<double>(kNsScale) / (sqrt(s) + eps));
+  __shared__ float shared_scale;
+  if (threadIdx.x < 32) {  // one warp a block: by every thread, one after another, the sums took 1.7 of 1.8 ms at 16 x 2048^2
+    double s = 0.0;
+    for (int c = static_cast<int>(threadIdx.x); c < chunks; c += 32)
+      s += __ldcg(part + static_cast<int64_t>(blockIdx.y) * chunks + c);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    if (threadIdx.x == 0) shared_scale = static_cast<float>(static_cast<double>(kNsScale) / (sqrt(s) + eps));
+  }
+  __syncthreads();
+  const float scale = shared_scale;
   const int per_row = ld / 8;
   const int64_t groups = static_cast<int64_t>(M) * per_row;
   const int64_t z = blockIdx.y;
@@ -385,48 +393,41 @@ struct NsCall {
   cudaStream_t stream;
 };
 
-template <bool kTall, int TN>
+template <bool kTall, bool kPair>
 static int ns_steps(const NsCall& n) {
   const NsLayout& L = n.L;
   const int S = L.side;
+  int rc = MOE_OK;
   auto xmap = [&](CUtensorMap* m, int64_t off, int b0, int b1) {
-    return make_map3(m, n.ws + off, Elem::F16, n.N, n.M, n.E, int64_t(L.ldx) * 2, int64_t(n.M) * L.ldx * 2, b0, b1, 1);
+    if (rc == MOE_OK)
+      rc = make_map3(m, n.ws + off, Elem::F16, n.N, n.M, n.E, int64_t(L.ldx) * 2, int64_t(n.M) * L.ldx * 2, b0, b1, 1);
   };
   auto smap = [&](CUtensorMap* m, int64_t off, int b0, int b1) {
-    return make_map3(m, n.ws + off, Elem::F16, S, S, n.E, int64_t(L.lds) * 2, int64_t(S) * L.lds * 2, b0, b1, 1);
+    if (rc == MOE_OK)
+      rc = make_map3(m, n.ws + off, Elem::F16, S, S, n.E, int64_t(L.lds) * 2, int64_t(S) * L.lds * 2, b0, b1, 1);
   };
-  // operands of the three products and the store form of every buffer
-  CUtensorMap xa[2], xb[2], xs_hi[2], xs_lo[2], xk[2], gram_a, gram_b, gram_s, poly_a, poly_b, poly_s, out_s;
-  int rc = MOE_OK;
-  for (int i = 0; i < 2 && rc == MOE_OK; ++i) {
-    if (kTall) {
-      rc = xmap(&xa[i], L.hi[i], 64, kGK);                          // X^T X: both MN-major
-      if (rc == MOE_OK) rc = xmap(&xk[i], L.hi[i], kGK, kGM);       // X B: K-major
-      xb[i] = xa[i];
-    } else {
-      rc = xmap(&xa[i], L.hi[i], kGK, kGM);                         // X X^T: both K-major
-      if (rc == MOE_OK) rc = xmap(&xb[i], L.hi[i], kGK, TN);
-      if (rc == MOE_OK) rc = xmap(&xk[i], L.hi[i], 64, kGK);        // B X: MN-major
-    }
-    if (rc == MOE_OK) rc = xmap(&xs_hi[i], L.hi[i], 32, 32);
-    if (rc == MOE_OK) rc = xmap(&xs_lo[i], L.lo[i], 32, 32);
+  // operands are read in boxes of 64 columns, 128 rows (K-major) or 64 (MN-major); pieces are stored, and read
+  // beside an accumulator, in boxes of 32 rows
+  CUtensorMap x_k[2], x_mn[2], hi32[2], lo32[2], gram_k, gram32, poly_k, poly32, out32;
+  for (int i = 0; i < 2; ++i) {
+    xmap(&x_k[i], L.hi[i], kGK, 128);
+    xmap(&x_mn[i], L.hi[i], 64, kGK);
+    xmap(&hi32[i], L.hi[i], 32, 32);
+    xmap(&lo32[i], L.lo[i], 32, 32);
   }
-  if (rc == MOE_OK) rc = smap(&gram_a, L.gram, kGK, kGM);
-  if (rc == MOE_OK) rc = smap(&gram_b, L.gram, kGK, TN);
-  if (rc == MOE_OK) rc = smap(&gram_s, L.gram, 64, 32);
-  if (rc == MOE_OK) rc = smap(&poly_a, L.poly, kGK, kGM);
-  if (rc == MOE_OK) rc = smap(&poly_b, L.poly, kGK, TN);
-  if (rc == MOE_OK) rc = smap(&poly_s, L.poly, 64, 32);
-  out_s = xs_hi[0];
+  smap(&gram_k, L.gram, kGK, 128);
+  smap(&gram32, L.gram, 32, 32);
+  smap(&poly_k, L.poly, kGK, 128);
+  smap(&poly32, L.poly, 32, 32);
+  out32 = hi32[0];
   if (rc == MOE_OK && !n.direct)
-    rc = make_map3(&out_s, n.out, Elem::Bf16, n.N, n.M, n.E, int64_t(n.N) * 2, int64_t(n.M) * n.N * 2, 32, 32, 1);
+    rc = make_map3(&out32, n.out, Elem::Bf16, n.N, n.M, n.E, int64_t(n.N) * 2, int64_t(n.M) * n.N * 2, 32, 32, 1);
   if (rc != MOE_OK) return rc;
 
   GemmParams base{};
   if ((rc = status_word(n.nm, &base.status)) != MOE_OK) return rc;
   base.wait_ns = kWaitTimeoutNs;
   base.batches = n.E;
-  base.a_rows = kGM;
   base.store_rows = 32;
   base.side = S;
   base.diag = reinterpret_cast<float*>(n.ws + L.diag);
@@ -434,46 +435,41 @@ static int ns_steps(const NsCall& n) {
   auto tiles = [&](GemmParams* p, int m, int cols, int k) {
     p->m_total = m;
     p->n_total = cols;
-    p->m_tiles = (m + kGM - 1) / kGM;
-    p->n_tiles = (cols + TN - 1) / TN;
+    p->m_tiles = (m + tile_m(kPair) - 1) / tile_m(kPair);
+    p->n_tiles = (cols + tile_n(kPair) - 1) / tile_n(kPair);
     p->nk = (k + kGK - 1) / kGK;
     return static_cast<int64_t>(n.E) * p->m_tiles * p->n_tiles;
   };
   for (int i = 0; i < n.steps; ++i) {
     const int cur = i & 1, nxt = cur ^ 1;
+    const CUtensorMap& x = kTall ? x_mn[cur] : x_k[cur];  // X^T X: both MN-major; X X^T: both K-major
     GemmParams p = base;
     int64_t units = tiles(&p, S, S, kTall ? n.M : n.N);
     p.alpha = 1.0f / (kNsScale * kNsScale);
-    rc = launch_tile_gemm<kTall ? Form::TN : Form::NT, Sched::Batch, Epi::Gram, TN, false>(
-        n.nm, xa[cur], xb[cur], gram_s, gram_s, p, units, true, n.stream);
+    rc = launch_tile_gemm<kTall ? Form::TN : Form::NT, Sched::Batch, Epi::Gram, kPair, false>(
+        n.nm, GemmMaps{x, x, gram32, gram32, gram32, gram32}, p, units, true, n.stream);
     if (rc != MOE_OK) return rc;
     p = base;
     units = tiles(&p, S, S, S);
     p.alpha = n.c;
     p.beta = n.b;
     p.use_diag = i >= kNsDiagFrom ? 1 : 0;
-    p.c0 = reinterpret_cast<const __half*>(n.ws + L.gram);
-    p.ldc = L.lds;
-    p.zc = int64_t(S) * L.lds;
-    rc = launch_tile_gemm<Form::NT, Sched::Batch, Epi::Poly, TN, false>(n.nm, gram_a, gram_b, poly_s, poly_s, p, units,
-                                                                       true, n.stream);
+    rc = launch_tile_gemm<Form::NT, Sched::Batch, Epi::Poly, kPair, false>(
+        n.nm, GemmMaps{gram_k, gram_k, poly32, poly32, gram32, gram32}, p, units, true, n.stream);
     if (rc != MOE_OK) return rc;
     p = base;
     units = tiles(&p, n.M, n.N, S);
     p.alpha = n.a;
     p.beta = 1.0f / kNsScale;
     p.use_diag = i >= kNsDiagFrom ? 1 : 0;
-    p.c0 = reinterpret_cast<const __half*>(n.ws + L.hi[cur]);
-    p.c1 = reinterpret_cast<const __half*>(n.ws + L.lo[cur]);
-    p.ldc = L.ldx;
-    p.zc = int64_t(n.M) * L.ldx;
     p.last = i + 1 == n.steps ? 1 : 0;
     p.direct = n.direct ? 1 : 0;
     p.out = static_cast<__nv_bfloat16*>(n.out);
-    rc = kTall ? launch_tile_gemm<Form::NT, Sched::Batch, Epi::Update, TN, false>(
-                     n.nm, xk[cur], poly_b, p.last ? out_s : xs_hi[nxt], xs_lo[nxt], p, units, true, n.stream)
-               : launch_tile_gemm<Form::NN, Sched::Batch, Epi::Update, TN, false>(
-                     n.nm, poly_a, xk[cur], p.last ? out_s : xs_hi[nxt], xs_lo[nxt], p, units, true, n.stream);
+    // X B, both K-major (B is symmetric), or B X
+    const GemmMaps u{kTall ? x_k[cur] : poly_k, kTall ? poly_k : x_mn[cur], p.last ? out32 : hi32[nxt], lo32[nxt],
+                     hi32[cur], lo32[cur]};
+    rc = launch_tile_gemm<kTall ? Form::NT : Form::NN, Sched::Batch, Epi::Update, kPair, false>(n.nm, u, p, units, true,
+                                                                                               n.stream);
     if (rc != MOE_OK) return rc;
   }
   return MOE_OK;
@@ -539,9 +535,9 @@ extern "C" int moe_orthogonalize(const void* g, int g_dtype, int E, int M, int N
                            static_cast<const double*>(part), n.L.chunks, static_cast<double>(eps),
                            reinterpret_cast<__half*>(n.ws + n.L.hi[0]), reinterpret_cast<__half*>(n.ws + n.L.lo[0]));
   if (err != cudaSuccess) return cuda_fail(nm, err);
-  // 256-column tiles where they fill the SMs, else 128 for twice as many
-  const int64_t t256 = int64_t(E) * ((M + kGM - 1) / kGM) * ((N + 255) / 256);
-  const bool wide_tiles = t256 >= sm_count();
-  if (M > N) return wide_tiles ? ns_steps<true, 256>(n) : ns_steps<true, 128>(n);
-  return wide_tiles ? ns_steps<false, 256>(n) : ns_steps<false, 128>(n);
+  // tiles of 256 x 256 on CTA pairs where they fill the SMs, else 128 x 128 for four times as many
+  const int64_t pairs = int64_t(E) * ((n.L.side + 255) / 256) * ((n.L.side + 255) / 256);
+  const bool pair = pairs >= sm_count() / 2;
+  if (M > N) return pair ? ns_steps<true, true>(n) : ns_steps<true, false>(n);
+  return pair ? ns_steps<false, true>(n) : ns_steps<false, false>(n);
 }

@@ -1,25 +1,41 @@
 // A persistent tcgen05 product of 16-bit operands, tile by tile, for the
-// training operators: D (128 x TN, fp32 in TMEM) = A . B over a contraction
-// cut into chunks of 64, in the three forms that a layer's forward pass and
-// its two gradients need,
+// training operators: D (fp32 in TMEM) = A . B over a contraction cut into
+// chunks of 64, in the three forms that a layer's forward pass and its two
+// gradients need,
 //   NT   D[i][j] = sum_k A[i][k] B[j][k]    both operands K-major
 //   NN   D[i][j] = sum_k A[i][k] B[k][j]    B is MN-major
 //   TN   D[i][j] = sum_k A[k][i] B[k][j]    both are MN-major
 // The tensor cores read either layout from shared memory (a bit each in the
 // instruction descriptor), so no operand is ever transposed in memory.
 //
+// Tiles.  kPair: two CTAs of a cluster work on one 256 x 256 tile with
+// cta_group::2 MMAs: each loads half of A's rows and half of B's, 32 KB a
+// chunk, and takes half of D's rows out of its own TMEM.  That is 128 flop a
+// byte from L2, where one CTA on a 128 x 256 tile has 85 and, at 8192 tokens
+// on 64 experts (K = N = 2048), took 484 us in isolation and 593 us under the
+// power cap, its tensor pipe 67 % busy waiting for operands.  Otherwise one
+// CTA works on 128 x 128: for experts with too few rows to fill 256, where the
+// weights' bytes bound the call and 148 CTAs stream more of them at once.
+//
 // One CTA per SM walks the tiles.  Warp 0 copies operand chunks by TMA into a
-// ring of stages, warp 1 issues the MMAs (one lane), warps 2-9 take a finished
-// accumulator out of TMEM (two of them alternate, so the epilogue of a tile
-// runs beside the next tile's MMAs), apply the epilogue and store it by TMA
-// from a swizzled staging buffer of 4 KB a warp.  Every wait is bounded.
+// ring of 5 stages, warp 1 (of the even CTA of a pair) issues the MMAs, one
+// lane; warps 2-9 take a finished accumulator out of TMEM (two of them
+// alternate, so the epilogue of a tile runs beside the next tile's MMAs) and
+// store it by TMA from two swizzled staging buffers of 4 KB a warp.  What an
+// epilogue reads beside the accumulator (h, the iterate, the Gram matrix) is
+// loaded by TMA into the staging buffer that its result then replaces, one
+// piece ahead: read by each thread from its own row, as the accumulator lies,
+// those loads took longer than the product.  Every wait is bounded.
 //
 // What a tile is (Sched):
-//   Blocks   a planner block of rows by TN columns of that block's expert;
-//   Experts  128 x TN of one expert's weight gradient, contracted over the
-//            expert's rows (a run of planner blocks; the rows behind the last
-//            routed one are cleared in shared memory, whatever they hold);
-//   Batch    128 x TN of one matrix of a batch.
+//   Blocks   rows of one expert (consecutive planner blocks, whatever block_m
+//            is) by columns of that expert's weights;
+//   Experts  a part of one expert's weight gradient, contracted over the
+//            expert's rows; what lies behind the last routed one in a chunk is
+//            cleared in shared memory by warp 10, whatever it holds;
+//   Batch    a part of one matrix of a batch; of a symmetric one (Gram, Poly)
+//            the tiles on and above the diagonal, each stored as it is and
+//            transposed.
 #pragma once
 
 #include <atomic>
@@ -33,34 +49,32 @@ namespace moe {
 enum class Form { NT, NN, TN };
 enum class Sched { Blocks, Experts, Batch };
 enum class Epi {
-  Rows,        // bf16 rows of a block
+  Rows,        // bf16 rows of an expert
   GateUp,      // h = [gate | up] and silu(gate) * up, bf16
   SwigluGrad,  // D is the gradient of act: bf16 gradients of gate and up
   Weights,     // a weight gradient, bf16 or fp32, the latter optionally added to what is there
   Gram,        // alpha * D, fp16
-  Poly,        // b * C + c * D, fp16, optionally with its diagonal taken out into fp32
+  Poly,        // beta * C + alpha * D, fp16, optionally with its diagonal taken out into fp32
   Update       // coefficient * (hi + lo / 2048) + D: the next iterate's hi and lo, or the result in bf16
 };
 
-constexpr int kGM = 128;
-constexpr int kGK = 64;
+constexpr int kGK = 64;     // contraction indices a chunk
 constexpr int kGRow = 128;  // bytes of an operand row in a stage
+constexpr int kGHalf = 128 * kGRow;   // bytes of a CTA's A, and of its B, a chunk
+constexpr int kGStage = 2 * kGHalf;
+constexpr int kGStages = 5;
 constexpr int kGEpiWarps = 8;
-constexpr int kGThreads = 32 * (2 + kGEpiWarps);
-constexpr int kGStaging = 4096;  // bytes a warp
-constexpr int kGSmemLimit = 232448;
+constexpr int kGPatchWarp = 2 + kGEpiWarps;
+constexpr int kGThreads = 32 * (3 + kGEpiWarps);
+constexpr int kGBuf = 4096;  // bytes of a staging buffer; two a warp
+constexpr int kGStaging = kGStages * kGStage;
+constexpr int kGCtrl = kGStaging + kGEpiWarps * 2 * kGBuf;
+constexpr int kGSmem = 1024 + kGCtrl + 512;
+static_assert(kGSmem <= 232448, "shared memory");
 constexpr float kLoScale = 2048.0f;  // lo = fp16(2048 * (value - hi)): 11 more bits
 
-template <int TN>
-struct GemmShape {
-  static constexpr int a_bytes = kGM * kGRow, b_bytes = TN * kGRow;
-  static constexpr int stage = a_bytes + b_bytes;
-  static constexpr int stages = TN == 256 ? 4 : 6;
-  static constexpr int staging = stages * stage;  // offset
-  static constexpr int ctrl = staging + kGEpiWarps * kGStaging;
-  static constexpr int smem = 1024 + ctrl + 256;
-  static_assert(smem <= kGSmemLimit, "shared memory");
-};
+constexpr int tile_m(bool pair) { return pair ? 256 : 128; }
+constexpr int tile_n(bool pair) { return pair ? 256 : 128; }
 
 struct GemmParams {
   // planner (Blocks, Experts)
@@ -70,22 +84,16 @@ struct GemmParams {
   int bm, max_blocks, E;
   // tiles
   int m_tiles, n_tiles, batches;
-  int m_total, n_total;  // rows (Experts, Batch) and columns of D
+  int m_total, n_total;  // rows (Experts, Batch) and columns of D; GateUp, SwigluGrad: columns of act
   int nk;                // chunks of the contraction (Blocks, Batch)
-  int a_rows;            // rows of A's box (K-major A)
-  int store_rows;        // rows of the store boxes
-  // SwigluGrad
-  const __nv_bfloat16* h;
+  int store_rows;        // rows of the store (and side) boxes
   // Weights
   int out_f32, accumulate;
-  // Gram, Poly, Update (read past L1: the launches are chained and reuse buffers)
+  // Gram, Poly, Update (scalars read past L1: the launches are chained and reuse buffers)
   float alpha, beta;
   int use_diag, tall, last, direct;
   float* diag;           // (batches, side)
   int side;
-  const __half* c0;      // Poly: the Gram matrix; Update: hi
-  const __half* c1;      // Update: lo
-  int64_t ldc, zc;       // row and matrix strides of c0 and c1, elements
   __nv_bfloat16* out;    // Update, last, direct: (batches, m_total, n_total)
   int* status;
   unsigned long long wait_ns;
@@ -107,8 +115,11 @@ __device__ __forceinline__ float2 unpack_f16(uint32_t w) {
 }
 
 struct Tile {
-  int z, m0, n0;
-  int nk;      // chunks; 0: a weight gradient without rows; < 0: nothing to do
+  int z;       // expert or matrix
+  int m0, n0;  // this CTA's first row of A, the tile's first column
+  int limit;   // rows of this CTA's half that belong to the output (<= 0: none)
+  int nk;      // chunks; 0: a weight gradient without rows
+  bool mirror; // symmetric: the transposed tile is stored too
   int p0;      // Experts: first row of the contraction
   int rows;    // Experts: its routed rows
 };
@@ -127,551 +138,692 @@ __device__ __forceinline__ int warp_lower_bound(const int32_t* ids, int n, int e
   return lo;
 }
 
-// The tiles of one role, in the order that every role walks them.
-template <Sched kSched, Epi kEpi, int TN>
+// The tiles of one role, in the order that every role walks them: tile numbers
+// `first`, first + stride, ... (warp-collective).
+template <Sched kSched, Epi kEpi, bool kPair>
 struct Walk {
+  static constexpr int kCols = kEpi == Epi::GateUp ? tile_n(kPair) / 2 : tile_n(kPair);
+  static constexpr bool kSym = kEpi == Epi::Gram || kEpi == Epi::Poly;  // square tiles, m_tiles == n_tiles
   const GemmParams& p;
-  const int lane;
-  int blocks, units;
+  const int lane, rank, stride;
+  int u, blocks, units, per_z;
+  // Blocks: a window of 32 blocks and those in it that begin a tile of their expert
+  int win = 0, before = 0, carry = 0, prev = -1, id = -1;
+  uint32_t heads = 0;
+  // Experts
   int z_seen = -1, seg_lo = 0, seg_rows = 0;
 
-  __device__ __forceinline__ Walk(const GemmParams& p_) : p(p_), lane(static_cast<int>(lane_id())) {
+  __device__ __forceinline__ Walk(const GemmParams& p_, int rank_)
+      : p(p_), lane(static_cast<int>(lane_id())), rank(rank_), stride(kPair ? gridDim.x / 2 : gridDim.x) {
+    u = kPair ? blockIdx.x / 2 : blockIdx.x;
     blocks = 0;
     if (kSched != Sched::Batch) {
       const int n = __ldg(p.ntpp) / p.bm;
       blocks = n < 0 ? 0 : min(n, p.max_blocks);
     }
-    units = kSched == Sched::Blocks ? blocks * p.n_tiles : p.batches * p.m_tiles * p.n_tiles;
+    per_z = kSym ? p.m_tiles * (p.m_tiles + 1) / 2 : p.m_tiles * p.n_tiles;
+    units = p.batches * per_z;
+    if (kSched == Sched::Blocks) look(0);
   }
 
-  __device__ __forceinline__ Tile at(int u) {
-    Tile t{};
-    constexpr int kCols = kEpi == Epi::GateUp ? TN / 2 : TN;
+  // The window from block `at` on: a tile begins every tile_m / bm blocks of an expert's run.
+  __device__ __forceinline__ void look(int at) {
+    win = at;
+    const int per = tile_m(kPair) / p.bm;
+    id = at + lane < blocks ? __ldg(p.expert_ids + at + lane) : -1;
+    const int left = __shfl_up_sync(0xffffffffu, id, 1);
+    const uint32_t starts = __ballot_sync(0xffffffffu, id != (lane ? left : prev));
+    const uint32_t mine = starts & (0xffffffffu >> (31 - lane));
+    const int pos = mine ? lane - (31 - __clz(static_cast<int>(mine))) : lane + carry;  // place in the run
+    heads = __ballot_sync(0xffffffffu, id >= 0 && id < p.E && pos % per == 0);
+    carry = __shfl_sync(0xffffffffu, pos, 31) + 1;
+    prev = __shfl_sync(0xffffffffu, id, 31);
+  }
+
+  __device__ __forceinline__ bool next(Tile* t) {
     if (kSched == Sched::Blocks) {
-      const int b = u / p.n_tiles;
-      t.z = __ldg(p.expert_ids + b);
-      t.m0 = b * p.bm;
-      t.n0 = (u - b * p.n_tiles) * kCols;
-      t.nk = t.z >= 0 && t.z < p.E ? p.nk : -1;
-      return t;
+      const int want = u / p.n_tiles;
+      while (want - before >= __popc(heads)) {
+        if (win + 32 >= blocks) return false;
+        before += __popc(heads);
+        look(win + 32);
+      }
+      const int at = static_cast<int>(__fns(heads, 0, want - before + 1));
+      const int b = win + at;
+      t->z = __shfl_sync(0xffffffffu, id, at);
+      t->n0 = (u - want * p.n_tiles) * kCols;
+      // blocks of the tile: those from b on with its expert
+      const int per = tile_m(kPair) / p.bm;
+      const uint32_t same = __ballot_sync(
+          0xffffffffu, lane < per && b + lane < blocks && __ldg(p.expert_ids + min(b + lane, blocks - 1)) == t->z);
+      const int run = same == 0xffffffffu ? 32 : __ffs(static_cast<int>(~same)) - 1;
+      t->m0 = b * p.bm + rank * 128;
+      t->limit = min(128, run * p.bm - rank * 128);
+      t->nk = p.nk;
+      t->p0 = t->rows = 0;
+      t->mirror = false;
+      u += stride;
+      return true;
     }
-    const int per = p.m_tiles * p.n_tiles;
-    t.z = u / per;
-    const int r = u - t.z * per, mi = r / p.n_tiles;
-    t.m0 = mi * kGM;
-    t.n0 = (r - mi * p.n_tiles) * kCols;
-    t.nk = p.nk;
+    if (u >= units) return false;
+    t->z = u / per_z;
+    int mi = 0, ni = u - t->z * per_z;
+    if (kSym) {
+      while (ni >= p.n_tiles - mi) ni -= p.n_tiles - mi++;
+      ni += mi;
+      t->mirror = ni != mi;
+    } else {
+      mi = ni / p.n_tiles;
+      ni -= mi * p.n_tiles;
+      t->mirror = false;
+    }
+    t->m0 = mi * tile_m(kPair) + rank * 128;
+    t->n0 = ni * kCols;
+    t->limit = min(128, p.m_total - t->m0);
+    t->nk = p.nk;
+    t->p0 = t->rows = 0;
     if (kSched == Sched::Experts) {
-      if (t.z != z_seen) {  // warp-uniform
-        z_seen = t.z;
-        seg_lo = warp_lower_bound(p.expert_ids, blocks, t.z, lane);
-        const int n = warp_lower_bound(p.expert_ids + seg_lo, blocks - seg_lo, t.z + 1, lane);
+      if (t->z != z_seen) {  // warp-uniform
+        z_seen = t->z;
+        seg_lo = warp_lower_bound(p.expert_ids, blocks, t->z, lane);
+        const int n = warp_lower_bound(p.expert_ids + seg_lo, blocks - seg_lo, t->z + 1, lane);
         seg_rows = 0;
         if (n > 0) {  // whole blocks, and the routed rows that the last one begins with
           const int64_t at = static_cast<int64_t>(seg_lo + n - 1) * p.bm;
           int last = 0;
-          for (int q = 0; q < p.bm; q += 32) {
-            bool v = false;
-            if (q + lane < p.bm) {
-              const int id = __ldg(p.sorted_ids + at + q + lane);
-              v = id >= 0;
-            }
-            last += __popc(__ballot_sync(0xffffffffu, v));
-          }
+          for (int q = 0; q < p.bm; q += 32)
+            last += __popc(__ballot_sync(0xffffffffu, q + lane < p.bm && __ldg(p.sorted_ids + at + min(q + lane, p.bm - 1)) >= 0));
           seg_rows = (n - 1) * p.bm + last;
         }
       }
-      t.p0 = seg_lo * p.bm;
-      t.rows = seg_rows;
-      t.nk = (seg_rows + kGK - 1) / kGK;
+      t->p0 = seg_lo * p.bm;
+      t->rows = seg_rows;
+      t->nk = (seg_rows + kGK - 1) / kGK;
     }
-    return t;
+    u += stride;
+    return true;
   }
 };
 
-template <Form kForm, Sched kSched, Epi kEpi, int TN, bool kBf16>
+// What a chunk of a weight gradient's contraction holds beyond the expert's
+// routed rows: from row `rem` of 64 on; 64 or more: nothing.
+__device__ __forceinline__ bool ragged(const Tile& t, int kc) { return t.rows - kc * kGK < kGK; }
+
+template <Form kForm, Sched kSched, Epi kEpi, bool kPair, bool kBf16>
 __global__ void __launch_bounds__(kGThreads, 1)
     tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                      const __grid_constant__ CUtensorMap tm_d, const __grid_constant__ CUtensorMap tm_d2,
+                     const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_c2,
                      const __grid_constant__ GemmParams p) {
-  using S = GemmShape<TN>;
+  constexpr int kN = tile_n(kPair);
+  constexpr uint32_t kTmemCols = 2 * kN;
+  constexpr bool kAMn = kForm == Form::TN, kBMn = kForm != Form::NT;
+  // epilogues that read a second operand (side tiles of 32 columns; one or two at once)
+  constexpr bool kSide = kEpi == Epi::SwigluGrad || kEpi == Epi::Poly || kEpi == Epi::Update;
+  constexpr int kSideTiles = kEpi == Epi::Poly ? 1 : 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::ctrl);
-  uint64_t* empty = full + S::stages;
-  uint64_t* acc_full = empty + S::stages;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kGCtrl);
+  uint64_t* empty = full + kGStages;
+  uint64_t* part = empty + kGStages;      // ragged chunks: landed, not yet cleared
+  uint64_t* acc_full = part + kGStages;
   uint64_t* acc_empty = acc_full + 2;
-  uint32_t* tmem_base_sm = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  uint64_t* side_full = acc_empty + 2;    // [kGEpiWarps][2]
+  uint32_t* tmem_base_sm = reinterpret_cast<uint32_t*>(side_full + 2 * kGEpiWarps);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_sm + 1);
-  constexpr uint32_t kTmemCols = 2 * TN;
-  constexpr bool kAMn = kForm == Form::TN, kBMn = kForm != Form::NT;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = kPair ? cluster_ctarank() : 0u;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return mbar_wait(bar, parity, abort_flag, p.status, p.wait_ns);
+  };
+  // a barrier that threads of the other CTA arrive on.  The acquire at cluster scope is dear: taken for every chunk,
+  // with a releasing arrival from the other CTA, it made a chunk of 256 x 256 x 64 cost 1.06 us.
+  auto wait_cluster = [&](uint64_t* bar, uint32_t parity) {
+    return mbar_wait<kPair>(bar, parity, abort_flag, p.status, p.wait_ns);
+  };
 
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S::stages; ++s) {
-      mbar_init(&full[s], 1);
+    for (int s = 0; s < kGStages; ++s) {
+      // pair: the even CTA's twice, for the copies of both, or warp 10 of each
+      mbar_init(&full[s], kPair ? 2 : 1);
       mbar_init(&empty[s], 1);
+      mbar_init(&part[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&acc_full[a], 1);
-      mbar_init(&acc_empty[a], kGEpiWarps);
+      mbar_init(&acc_empty[a], kPair ? 2 * kGEpiWarps : kGEpiWarps);
     }
+    for (int i = 0; i < 2 * kGEpiWarps; ++i) mbar_init(&side_full[i], 1);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&tm_a);
     prefetch_tmap(&tm_b);
     prefetch_tmap(&tm_d);
+    if (kSide) prefetch_tmap(&tm_c);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_base_sm, kTmemCols);
-    tmem_relinquish();
+    if (kPair) {
+      tmem_alloc_pair(tmem_base_sm, kTmemCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_base_sm, kTmemCols);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if (kPair) cluster_sync();  // the other CTA's barriers are ready
   tc_fence_after();
   const uint32_t tbase = *tmem_base_sm;
   pdl_wait();  // what a chained launch before this one wrote is read below
-  Walk<kSched, kEpi, TN> walk(p);
+  Walk<kSched, kEpi, kPair> walk(p, static_cast<int>(rank));
+  Tile t;
 
   if (warp == 0) {
     // ------------------------------------------------ TMA producer
     const uint64_t pol = policy_evict_normal();
-    const uint32_t tx = static_cast<uint32_t>((kAMn ? kGM : p.a_rows) * kGRow + S::b_bytes);
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < walk.units && ok; u += gridDim.x) {
-      const Tile t = walk.at(u);
+    while (ok && walk.next(&t)) {
       const int za = kSched == Sched::Batch ? t.z : 0;
       const int zb = kSched == Sched::Experts ? 0 : t.z;
+      const int r = static_cast<int>(rank);
       for (int kc = 0; kc < t.nk; ++kc) {
         if (lane == 0) {
-          ok = mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.status, p.wait_ns);
+          ok = wait(&empty[s], ph ^ 1u);
           if (ok) {
-            uint8_t* a = smem + s * S::stage;
-            uint8_t* b = a + S::a_bytes;
+            uint8_t* a = smem + s * kGStage;
+            uint8_t* b = a + kGHalf;
             const int k0 = t.p0 + kc * kGK;
-            mbar_arrive_expect_tx(&full[s], tx);
+            const bool held = kSched == Sched::Experts && ragged(t, kc);
+            const uint32_t bar = held || !kPair ? smem_u32(held ? &part[s] : &full[s]) : cluster_addr(&full[s], 0);
+            if (held) {
+              mbar_arrive_expect_tx(&part[s], kGStage);
+            } else if (rank == 0) {  // the odd CTA's copies complete on the even one's barrier
+              mbar_arrive_expect_tx(&full[s], kPair ? 2 * kGStage : kGStage);
+              if (kPair) mbar_arrive(&full[s]);
+            }
+            auto load = [&](void* dst, const CUtensorMap* map, int c0, int c1, int c2) {
+              if (kPair)
+                tma_load_3d_pair(dst, map, bar, c0, c1, c2, pol);
+              else
+                tma_load_3d(dst, map, held ? &part[s] : &full[s], c0, c1, c2, pol);
+            };
             if (kAMn) {
-#pragma unroll
-              for (int i = 0; i < kGM / 64; ++i)
-                tma_load_3d(a + i * 64 * kGRow, &tm_a, &full[s], t.m0 + 64 * i, k0, za, pol);
+              load(a, &tm_a, t.m0, k0, za);
+              load(a + kGHalf / 2, &tm_a, t.m0 + 64, k0, za);
             } else {
-              tma_load_3d(a, &tm_a, &full[s], k0, t.m0, za, pol);
+              load(a, &tm_a, k0, t.m0, za);
             }
             if (kBMn) {
-#pragma unroll
-              for (int i = 0; i < TN / 64; ++i)
-                tma_load_3d(b + i * 64 * kGRow, &tm_b, &full[s], t.n0 + 64 * i, k0, zb, pol);
+              load(b, &tm_b, t.n0 + 128 * r, k0, zb);
+              load(b + kGHalf / 2, &tm_b, t.n0 + 128 * r + 64, k0, zb);
             } else if (kEpi == Epi::GateUp) {
-              tma_load_3d(b, &tm_b, &full[s], k0, t.n0, 2 * zb, pol);
-              tma_load_3d(b + S::b_bytes / 2, &tm_b, &full[s], k0, t.n0, 2 * zb + 1, pol);
+              if (kPair) {  // the even CTA holds the gate columns, the odd one the up columns
+                load(b, &tm_b, k0, t.n0, 2 * zb + r);
+              } else {
+                load(b, &tm_b, k0, t.n0, 2 * zb);
+                load(b + kGHalf / 2, &tm_b, k0, t.n0, 2 * zb + 1);
+              }
             } else {
-              tma_load_3d(b, &tm_b, &full[s], k0, t.n0, zb, pol);
+              load(b, &tm_b, k0, t.n0 + 128 * r, zb);
             }
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
-        if (++s == S::stages) { s = 0; ph ^= 1u; }
+        if (++s == kGStages) { s = 0; ph ^= 1u; }
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer
-    constexpr uint32_t kIdesc = idesc_f16(kGM, TN, kBf16, kAMn, kBMn);
+    constexpr uint32_t kIdesc = idesc_f16(tile_m(kPair), kN, kBf16, kAMn, kBMn);
     int s = 0, acc_it = 0;
     uint32_t ph = 0;
-    bool ok = true;
-    for (int u = blockIdx.x; u < walk.units && ok; u += gridDim.x) {
-      const Tile t = walk.at(u);
-      if (t.nk <= 0) continue;
+    bool ok = rank == 0;
+    while (ok && walk.next(&t)) {
+      if (t.nk == 0) continue;
       const int buf = acc_it & 1;
-      if (lane == 0)
-        ok = mbar_wait(&acc_empty[buf], ((acc_it >> 1) & 1) ^ 1u, abort_flag, p.status, p.wait_ns);
+      if (lane == 0) ok = wait_cluster(&acc_empty[buf], ((acc_it >> 1) & 1) ^ 1u);
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t d = tbase + static_cast<uint32_t>(buf) * TN;
+      const uint32_t d = tbase + static_cast<uint32_t>(buf) * kN;
       for (int kc = 0; kc < t.nk; ++kc) {
-        uint8_t* a = smem + s * S::stage;
-        uint8_t* b = a + S::a_bytes;
-        if (lane == 0) ok = mbar_wait(&full[s], ph, abort_flag, p.status, p.wait_ns);
+        if (lane == 0) {
+          ok = kSched == Sched::Experts && ragged(t, kc) ? wait_cluster(&full[s], ph) : wait(&full[s], ph);
+          if (ok) {
+            tc_fence_after();
+            const uint32_t a = smem_u32(smem + s * kGStage), b = a + kGHalf;
+            const uint64_t ad = kAMn ? sdesc_sw128_mn(a, kGHalf / 2) : sdesc_sw128(a);
+            const uint64_t bd = kBMn ? sdesc_sw128_mn(b, kGHalf / 2) : sdesc_sw128(b);
+            // whole steps without a routed row are left out
+            const int steps = kSched == Sched::Experts && ragged(t, kc) ? (t.rows - kc * kGK + 15) / 16 : kGK / 16;
+#pragma unroll
+            for (int kk = 0; kk < kGK / 16; ++kk) {
+              if (kSched == Sched::Experts && kk >= steps) break;
+              // 16 contraction indices: 32 bytes of a K-major row, 16 rows of an MN-major one
+              const uint64_t ak = ad + (kAMn ? 128u : 2u) * kk, bk = bd + (kBMn ? 128u : 2u) * kk;
+              if (kPair)
+                mma_f16_pair(d, ak, bk, kIdesc, (kc | kk) != 0);
+              else
+                mma_f16(d, ak, bk, kIdesc, (kc | kk) != 0);
+            }
+            if (kPair)
+              tc_commit_pair(&empty[s]);
+            else
+              tc_commit(&empty[s]);
+          }
+        }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
-        int kk_end = kGK / 16;
-        if (kSched == Sched::Experts) {
-          // the last chunk may reach past the expert's routed rows: what
-          // padding or another expert left there becomes zeros (a product
-          // with zero would keep a NaN), and whole steps of it are left out
-          const int rem = t.rows - kc * kGK;
-          if (rem < kGK) {
-            kk_end = (rem + 15) / 16;
-            __syncwarp();
-            const int gap = kk_end * 16 - rem;  // < 16 rows
-            constexpr int kBoxes = kGM / 64 + TN / 64;
-            for (int i = lane; i < kBoxes * gap * 8; i += 32) {
-              const int box = i / (gap * 8), r = i - box * (gap * 8);
-              *reinterpret_cast<uint4*>(a + box * 64 * kGRow + (rem + r / 8) * kGRow + (r & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-        }
-        if (lane == 0) {
-          tc_fence_after();
-          const uint64_t ad = kAMn ? sdesc_sw128_mn(smem_u32(a), 64 * kGRow) : sdesc_sw128(smem_u32(a));
-          const uint64_t bd = kBMn ? sdesc_sw128_mn(smem_u32(b), 64 * kGRow) : sdesc_sw128(smem_u32(b));
-#pragma unroll
-          for (int kk = 0; kk < kGK / 16; ++kk) {
-            if (kSched == Sched::Experts && kk >= kk_end) break;
-            // 16 contraction indices: 32 bytes of a K-major row, 16 rows of an MN-major one
-            mma_f16(d, ad + (kAMn ? 128u : 2u) * kk, bd + (kBMn ? 128u : 2u) * kk, kIdesc, (kc | kk) != 0);
-          }
-          tc_commit(&empty[s]);
-        }
-        __syncwarp();
-        if (++s == S::stages) { s = 0; ph ^= 1u; }
+        if (++s == kGStages) { s = 0; ph ^= 1u; }
       }
-      if (ok && lane == 0) tc_commit(&acc_full[buf]);
+      if (ok && lane == 0) {
+        if (kPair)
+          tc_commit_pair(&acc_full[buf]);
+        else
+          tc_commit(&acc_full[buf]);
+      }
       ++acc_it;
+    }
+  } else if (warp == kGPatchWarp) {
+    // ------------------------------------------------ rows behind the routed ones
+    // Padding, or another expert's rows, in an expert's last chunk become
+    // zeros (a product with zero would keep a NaN), up to the MMA's next 16.
+    if (kSched == Sched::Experts) {
+      int count = 0;
+      uint32_t seen = 0;  // parity of part[s], one bit a stage
+      bool ok = true;
+      while (ok && walk.next(&t)) {
+        if (t.nk > 0 && ragged(t, t.nk - 1)) {
+          const int s = (count + t.nk - 1) % kGStages;
+          ok = wait(&part[s], (seen >> s) & 1u);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          seen ^= 1u << s;
+          const int rem = t.rows - (t.nk - 1) * kGK;
+          const int gap = (rem + 15) / 16 * 16 - rem;
+          uint8_t* base = smem + s * kGStage;  // A, B: two boxes each of 64 rows of 128 bytes
+          for (int i = lane; i < 4 * gap * 8; i += 32) {
+            const int box = i / (gap * 8), r = i - box * (gap * 8);
+            *reinterpret_cast<uint4*>(base + box * (kGHalf / 2) + (rem + r / 8) * kGRow + (r & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (kPair)
+              mbar_arrive_cluster(cluster_addr(&full[s], 0));
+            else
+              mbar_arrive(&full[s]);
+          }
+        }
+        count += t.nk;
+      }
     }
   } else {
     // ------------------------------------------------ epilogue
     // Warp w reads TMEM lanes 32 (w % 4) .. + 31, a row a thread, and half of
-    // the tile's columns.
+    // the tile's columns, in pieces that fill a staging buffer.
     const int q = warp & 3, hf = (warp - 2) >> 2;
     const int r = 32 * q + lane;
-    const uint32_t stg = smem_u32(smem + S::staging + (warp - 2) * kGStaging);
+    constexpr int kHalfCols = kN / 2;
+    const uint32_t stg0 = smem_u32(smem + kGStaging + (warp - 2) * 2 * kGBuf);
+    uint64_t* side = side_full + (warp - 2) * 2;
+    int piece = 0;  // pieces so far; piece % 2 is the buffer
+    auto buffer = [&] { return stg0 + static_cast<uint32_t>(piece & 1) * kGBuf; };
     // 16 bytes of this thread's row of a staging tile, swizzled as its tensor
-    // map says: 128-byte rows (64 16-bit columns), or 64-byte rows (32 columns)
-    auto put128 = [&](int i, uint4 v) {
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stg + lane * 128 + ((i ^ (lane & 7)) << 4)),
-                   "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+    // map says: 128-byte rows, or 64-byte rows (two tiles a buffer)
+    auto at128 = [&](int i) { return buffer() + lane * 128 + ((i ^ (lane & 7)) << 4); };
+    auto at64 = [&](int tile, int i) { return buffer() + tile * 2048 + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4); };
+    auto put = [&](uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+    };
+    auto get = [&](uint32_t at, uint32_t (&v)[4]) {
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                   : "r"(at)
                    : "memory");
     };
-    auto put64 = [&](int tile, int i, uint4 v) {
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stg + tile * 2048 + lane * 64 +
-                                                                  ((i ^ ((lane >> 1) & 3)) << 4)),
-                   "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                   : "memory");
+    // a 32 x 32 piece in fp16 (w: this row's pairs) into the buffer's second tile, transposed: lanes 2i and
+    // 2i + 1 exchange halves and write a pair each, to rows 2j and 2j + 1, without bank conflicts
+    auto put_transposed = [&](const uint32_t (&w)[16]) {
+      const bool odd = lane & 1;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, w[j], 1);
+        const uint32_t pair = odd ? __byte_perm(other, w[j], 0x7632) : __byte_perm(w[j], other, 0x5410);
+        const uint32_t at = buffer() + 2048 + (2 * j + (odd ? 1 : 0)) * 64 + (((lane >> 3) ^ (j & 3)) << 4) + ((lane >> 1) & 3) * 4;
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(pair) : "memory");
+      }
     };
-    auto staging_free = [&] {
-      if (lane == 0) bulk_wait_read();
+    // the buffer about to be filled was last stored from two pieces ago
+    auto buffer_free = [&] {
+      if (lane == 0) bulk_wait_read<1>();
       __syncwarp();
     };
-    auto staged = [&] {
+    // a tile of the buffer to `map`: this warp's rows below the limit, boxes of store_rows
+    auto store = [&](const CUtensorMap* map, int off, int row_bytes, int c0, int c1, bool row_last) {
+      for (int i = 0; i < 32; i += p.store_rows) {
+        if (32 * q + i >= t.limit) break;
+        const uint32_t src = buffer() + off + i * row_bytes;
+        const int row = t.m0 + 32 * q + i;
+        if (kEpi == Epi::Weights && p.accumulate)
+          tma_add_3d(map, src, c0, row, c1);
+        else if (row_last)
+          tma_store_3d(map, src, c0, c1, row);
+        else
+          tma_store_3d(map, src, c0, row, c1);
+      }
+    };
+    auto stored = [&](auto f) {  // fills done by the lanes; f: the stores, by one
       fence_proxy_async_smem();
       __syncwarp();
-    };
-    // rows of this warp's 32 that are stored: those of the block, or of the matrix
-    auto store = [&](const CUtensorMap* map, int tile_off, int row_bytes, int m0, int limit, int c0, int c1_or_row,
-                     int z, bool row_last, bool add) {
       if (lane == 0) {
-        for (int i = 0; i < 32; i += p.store_rows) {
-          if (32 * q + i >= limit) break;
-          const uint32_t src = stg + tile_off + i * row_bytes;
-          const int row = m0 + 32 * q + i;
-          if (add)
-            tma_add_3d(map, src, c0, row, z);
-          else if (row_last)
-            tma_store_3d(map, src, c0, c1_or_row, row);
-          else
-            tma_store_3d(map, src, c0, row, z);
-        }
+        f();
         bulk_commit();
       }
+      ++piece;
     };
-    int acc_it = 0;
-    bool ok = true;
-    for (int u = blockIdx.x; u < walk.units && ok; u += gridDim.x) {
-      const Tile t = walk.at(u);
-      if (t.nk < 0 || (t.nk == 0 && p.accumulate)) continue;
-      // rows of the tile that belong to the output, and whether this thread's carries a value
-      const int limit = kSched == Sched::Blocks ? p.bm : min(kGM, p.m_total - t.m0);
-      bool mine = r < limit;
-      if (kSched == Sched::Blocks && mine) {
-        const int id = __ldg(p.sorted_ids + static_cast<int64_t>(t.m0) + r);
-        mine = id >= 0;
-      }
-      const int half = p.n_total;  // GateUp, SwigluGrad: columns of gate (and of up)
-      uint4 hg[4], hu[4];
-      auto load_h = [&](int col) {  // 32 columns of gate and up of this thread's row
-        const __nv_bfloat16* row = p.h + (static_cast<int64_t>(t.m0) + r) * 2 * half + col;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          hg[i] = hu[i] = make_uint4(0, 0, 0, 0);
-          if (mine && col + 8 * i < half) {
-            hg[i] = __ldg(reinterpret_cast<const uint4*>(row) + i);
-            hu[i] = __ldg(reinterpret_cast<const uint4*>(row + half) + i);
+    // Side tiles of the 32-column piece `col` into buffer b: from tm_c and tm_c2,
+    // except h, whose gate and up halves are two planes of one map.
+    auto side_load = [&](int b, int col) {
+      if (lane == 0) {
+        bulk_wait_read<0>();
+        int boxes = 0;
+        for (int i = 0; i < 32 && 32 * q + i < t.limit; i += p.store_rows) ++boxes;
+        mbar_arrive_expect_tx(&side[b], boxes * p.store_rows * 64 * kSideTiles);
+        const uint64_t pol = policy_evict_normal();
+        for (int i = 0; i < boxes; ++i) {
+          const int row = t.m0 + 32 * q + i * p.store_rows;
+          uint8_t* dst = smem + kGStaging + (warp - 2) * 2 * kGBuf + b * kGBuf + i * p.store_rows * 64;
+          if (kEpi == Epi::SwigluGrad) {
+            tma_load_3d(dst, &tm_c, &side[b], col, 0, row, pol);
+            tma_load_3d(dst + 2048, &tm_c, &side[b], col, 1, row, pol);
+          } else {
+            tma_load_3d(dst, &tm_c, &side[b], col, row, t.z, pol);
+            if (kSideTiles == 2) tma_load_3d(dst + 2048, &tm_c2, &side[b], col, row, t.z, pol);
           }
         }
-      };
-      if (kEpi == Epi::SwigluGrad) load_h(t.n0 + hf * (TN / 2));
+      }
+      __syncwarp();
+    };
+    int acc_it = 0;
+    uint32_t side_ph = 0;  // parity of side[b], a bit each
+    bool ok = true;
+    while (ok && walk.next(&t)) {
+      if (t.nk == 0 && p.accumulate) continue;
+      const bool rows_here = 32 * q < t.limit;  // warp-uniform
+      const int col0 = t.n0 + (kEpi == Epi::GateUp ? hf * (kHalfCols / 2) : hf * kHalfCols);
+      bool mine = r < t.limit;  // this thread's row carries a value (a padding row: zeros)
+      if (kSched == Sched::Blocks && mine) mine = __ldg(p.sorted_ids + static_cast<int64_t>(t.m0) + r) >= 0;
+      if (kSide && rows_here && col0 < p.n_total) side_load(piece & 1, col0);
       const int buf = acc_it & 1;
       if (t.nk > 0) {
-        ok = mbar_wait(&acc_full[buf], (acc_it >> 1) & 1, abort_flag, p.status, p.wait_ns);
+        ok = wait(&acc_full[buf], (acc_it >> 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
       }
-      const uint32_t tacc = tbase + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(buf) * TN;
-      if (32 * q < limit) {  // warp-uniform
-        if (kEpi == Epi::GateUp) {
-          const int col = t.n0 + 64 * hf;
-          if (col < half) {
-#pragma unroll 1
-            for (int part = 0; part < 2; ++part) {  // gate, then up, into h
-              staging_free();
+      const uint32_t tacc = tbase + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(buf) * kN;
+      auto acc32 = [&](int col, uint32_t (&v)[32]) {  // 32 columns of the accumulator, zeros without one
+        if (kSched != Sched::Experts || t.nk > 0) {
+          tmem_ld32(tacc + col, v);
+          tmem_ld_wait();
+        } else {
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                uint32_t v[32];
-                tmem_ld32(tacc + part * (TN / 2) + 64 * hf + 32 * c, v);
-                tmem_ld_wait();
+          for (int i = 0; i < 32; ++i) v[i] = 0;
+        }
+      };
+      if (rows_here) {
+        if (kEpi == Epi::GateUp) {
+#pragma unroll 1
+          for (int c = 0; c < kHalfCols / 64; ++c) {
+            const int col = col0 + 32 * c, ac = hf * (kHalfCols / 2) + 32 * c;
+            if (col >= p.n_total) break;
+            uint32_t g[32], up[32];
+            tmem_ld32(tacc + ac, g);
+            tmem_ld32(tacc + kN / 2 + ac, up);
+            tmem_ld_wait();
+            buffer_free();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t wg[4], wu[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int e = 8 * i + 2 * j;
+                wg[j] = mine ? pack_b16(__uint_as_float(g[e]), __uint_as_float(g[e + 1])) : 0u;
+                wu[j] = mine ? pack_b16(__uint_as_float(up[e]), __uint_as_float(up[e + 1])) : 0u;
+              }
+              put(at64(0, i), wg[0], wg[1], wg[2], wg[3]);
+              put(at64(1, i), wu[0], wu[1], wu[2], wu[3]);
+            }
+            stored([&] {
+              store(&tm_d, 0, 64, col, 0, true);
+              store(&tm_d, 2048, 64, col, 1, true);
+            });
+            buffer_free();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int e = 8 * i + 2 * j;
+                w[j] = mine ? pack_b16(silu_f32(__uint_as_float(g[e])) * __uint_as_float(up[e]),
+                                       silu_f32(__uint_as_float(g[e + 1])) * __uint_as_float(up[e + 1]))
+                            : 0u;
+              }
+              put(at64(0, i), w[0], w[1], w[2], w[3]);
+            }
+            stored([&] { store(&tm_d2, 0, 64, col, 0, false); });
+          }
+        } else if (kSide) {
+#pragma unroll 1
+          for (int c = 0; c < kHalfCols / 32; ++c) {
+            const int col = col0 + 32 * c;
+            if (col >= p.n_total) break;
+            const int b = piece & 1;
+            if (c + 1 < kHalfCols / 32 && col + 32 < p.n_total) side_load(b ^ 1, col + 32);
+            uint32_t v[32];
+            acc32(hf * kHalfCols + 32 * c, v);
+            ok = mbar_wait(&side[b], (side_ph >> b) & 1u, abort_flag, p.status, p.wait_ns);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            side_ph ^= 1u << b;
+            if (kEpi == Epi::SwigluGrad) {
+              // act = gate s(gate) up, s the sigmoid: d act / d gate = up s (1 + gate (1 - s)), d act / d up = gate s
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t gw[4], uw[4], og[4], ou[4];
+                get(at64(0, i), gw);
+                get(at64(1, i), uw);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const float2 g2 = unpack_b16(gw[j]), u2 = unpack_b16(uw[j]);
+                  float dg[2], du[2];
+#pragma unroll
+                  for (int k = 0; k < 2; ++k) {
+                    const float g = k ? g2.y : g2.x, up = k ? u2.y : u2.x;
+                    const float ga = __uint_as_float(v[8 * i + 2 * j + k]);
+                    const float sg = __fdividef(1.0f, 1.0f + __expf(-g));
+                    dg[k] = ga * up * sg * fmaf(g, 1.0f - sg, 1.0f);
+                    du[k] = ga * g * sg;
+                  }
+                  og[j] = mine ? pack_b16(dg[0], dg[1]) : 0u;
+                  ou[j] = mine ? pack_b16(du[0], du[1]) : 0u;
+                }
+                put(at64(0, i), og[0], og[1], og[2], og[3]);
+                put(at64(1, i), ou[0], ou[1], ou[2], ou[3]);
+              }
+              stored([&] {
+                store(&tm_d, 0, 64, col, 0, true);
+                store(&tm_d, 2048, 64, col, 1, true);
+              });
+            } else if (kEpi == Epi::Poly) {
+              uint32_t w[16];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t cw[4];
+                get(at64(0, i), cw);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const float2 c2 = unpack_f16(cw[j]);
+                  float o[2];
+#pragma unroll
+                  for (int k = 0; k < 2; ++k) {
+                    const int e = 8 * i + 2 * j + k;
+                    o[k] = fmaf(p.beta, k ? c2.y : c2.x, p.alpha * __uint_as_float(v[e]));
+                    if (p.use_diag && col + e == t.m0 + r) {
+                      if (mine) p.diag[static_cast<int64_t>(t.z) * p.side + t.m0 + r] = o[k];
+                      o[k] = 0.f;
+                    }
+                  }
+                  w[4 * i + j] = pack_f16(o[0], o[1]);
+                }
+                put(at64(0, i), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+              }
+              if (t.mirror) put_transposed(w);
+              stored([&] {
+                store(&tm_d, 0, 64, col, t.z, false);
+                if (t.mirror) tma_store_3d(&tm_d, buffer() + 2048, t.m0 + 32 * q, col, t.z);
+              });
+            } else {
+              const float* diag = p.diag + static_cast<int64_t>(t.z) * p.side;
+              float coef = p.alpha;
+              if (p.use_diag && !p.tall && mine) coef += __ldcg(diag + t.m0 + r);
+              // column col + lane's term of the tall form, handed round below
+              const float dcol = p.use_diag && p.tall ? __ldcg(diag + min(col + lane, p.side - 1)) : 0.f;
+              float y[32];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t hw[4], lw[4];
+                get(at64(0, i), hw);
+                get(at64(1, i), lw);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const float2 h2 = unpack_f16(hw[j]), l2 = unpack_f16(lw[j]);
+#pragma unroll
+                  for (int k = 0; k < 2; ++k) {
+                    const int e = 8 * i + 2 * j + k;
+                    const float x = fmaf(k ? l2.y : l2.x, 1.0f / kLoScale, k ? h2.y : h2.x);
+                    y[e] = fmaf(coef + __shfl_sync(0xffffffffu, dcol, e), x, __uint_as_float(v[e]));
+                  }
+                }
+              }
+              if (p.last && p.direct) {
+                __nv_bfloat16* dst = p.out + (static_cast<int64_t>(t.z) * p.m_total + t.m0 + r) * p.n_total + col;
+                if (mine) {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    if (col + e < p.n_total) dst[e] = __float2bfloat16_rn(y[e] * p.beta);
+                }
+                __syncwarp();  // the buffer is loaded into again
+                ++piece;
+              } else if (p.last) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                   uint32_t w[4];
 #pragma unroll
                   for (int j = 0; j < 4; ++j)
-                    w[j] = mine ? pack_b16(__uint_as_float(v[8 * i + 2 * j]), __uint_as_float(v[8 * i + 2 * j + 1])) : 0u;
-                  put128(4 * c + i, make_uint4(w[0], w[1], w[2], w[3]));
+                    w[j] = pack_b16(y[8 * i + 2 * j] * p.beta, y[8 * i + 2 * j + 1] * p.beta);
+                  put(at64(0, i), w[0], w[1], w[2], w[3]);
                 }
-              }
-              staged();
-              store(&tm_d, 0, 128, t.m0, limit, col, part, 0, true, false);
-            }
-            staging_free();
+                stored([&] { store(&tm_d, 0, 64, col, t.z, false); });
+              } else {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint32_t g[32], up[32];
-              tmem_ld32(tacc + 64 * hf + 32 * c, g);
-              tmem_ld32(tacc + TN / 2 + 64 * hf + 32 * c, up);
-              tmem_ld_wait();
+                for (int i = 0; i < 4; ++i) {
+                  uint32_t wh[4], wl[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint32_t w[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const int e = 8 * i + 2 * j;
-                  w[j] = mine ? pack_b16(silu_f32(__uint_as_float(g[e])) * __uint_as_float(up[e]),
-                                         silu_f32(__uint_as_float(g[e + 1])) * __uint_as_float(up[e + 1]))
-                              : 0u;
+                  for (int j = 0; j < 4; ++j) {
+                    const int e = 8 * i + 2 * j;
+                    wh[j] = pack_f16(y[e], y[e + 1]);
+                    const float2 h2 = unpack_f16(wh[j]);
+                    wl[j] = pack_f16((y[e] - h2.x) * kLoScale, (y[e + 1] - h2.y) * kLoScale);
+                  }
+                  put(at64(0, i), wh[0], wh[1], wh[2], wh[3]);
+                  put(at64(1, i), wl[0], wl[1], wl[2], wl[3]);
                 }
-                put128(4 * c + i, make_uint4(w[0], w[1], w[2], w[3]));
+                stored([&] {
+                  store(&tm_d, 0, 64, col, t.z, false);
+                  store(&tm_d2, 2048, 64, col, t.z, false);
+                });
               }
-            }
-            staged();
-            store(&tm_d2, 0, 128, t.m0, limit, col, 0, 0, false, false);
-          }
-        } else if (kEpi == Epi::SwigluGrad) {
-          // act = gate s(gate) up, s the sigmoid: d act / d gate = up s (1 + gate (1 - s)), d act / d up = gate s
-#pragma unroll 1
-          for (int c = 0; c < TN / 64; ++c) {
-            const int col = t.n0 + hf * (TN / 2) + 32 * c;
-            if (col >= half) break;
-            uint32_t v[32];
-            tmem_ld32(tacc + hf * (TN / 2) + 32 * c, v);
-            tmem_ld_wait();
-            staging_free();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t gw[4] = {hg[i].x, hg[i].y, hg[i].z, hg[i].w};
-              const uint32_t uw[4] = {hu[i].x, hu[i].y, hu[i].z, hu[i].w};
-              uint32_t og[4], ou[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float2 g2 = unpack_b16(gw[j]), u2 = unpack_b16(uw[j]);
-                float dg[2], du[2];
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                  const float g = b ? g2.y : g2.x, up = b ? u2.y : u2.x;
-                  const float ga = __uint_as_float(v[8 * i + 2 * j + b]);
-                  const float sg = __fdividef(1.0f, 1.0f + __expf(-g));
-                  dg[b] = ga * up * sg * fmaf(g, 1.0f - sg, 1.0f);
-                  du[b] = ga * g * sg;
-                }
-                og[j] = mine ? pack_b16(dg[0], dg[1]) : 0u;
-                ou[j] = mine ? pack_b16(du[0], du[1]) : 0u;
-              }
-              put64(0, i, make_uint4(og[0], og[1], og[2], og[3]));
-              put64(1, i, make_uint4(ou[0], ou[1], ou[2], ou[3]));
-            }
-            if (c + 1 < TN / 64) load_h(col + 32);
-            staged();
-            store(&tm_d, 0, 64, t.m0, limit, col, 0, 0, true, false);
-            store(&tm_d, 2048, 64, t.m0, limit, col, 1, 0, true, false);
-          }
-        } else if (kEpi == Epi::Update) {
-          const __half* hi_row = p.c0 + t.z * p.zc + (static_cast<int64_t>(t.m0) + r) * p.ldc;
-          const __half* lo_row = p.c1 + t.z * p.zc + (static_cast<int64_t>(t.m0) + r) * p.ldc;
-          const float* diag = p.diag + static_cast<int64_t>(t.z) * p.side;
-          float coef = p.alpha;
-          if (p.use_diag && !p.tall && mine) coef += __ldcg(diag + t.m0 + r);
-#pragma unroll 1
-          for (int c = 0; c < TN / 64; ++c) {
-            const int col = t.n0 + hf * (TN / 2) + 32 * c;
-            if (col >= p.n_total) break;
-            uint4 hi[4], lo[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              hi[i] = lo[i] = make_uint4(0, 0, 0, 0);
-              if (mine && col + 8 * i < p.n_total) {  // rows are padded to 8 elements
-                hi[i] = __ldcg(reinterpret_cast<const uint4*>(hi_row + col) + i);
-                lo[i] = __ldcg(reinterpret_cast<const uint4*>(lo_row + col) + i);
-              }
-            }
-            uint32_t v[32];
-            tmem_ld32(tacc + hf * (TN / 2) + 32 * c, v);
-            tmem_ld_wait();
-            float y[32];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t hw[4] = {hi[i].x, hi[i].y, hi[i].z, hi[i].w};
-              const uint32_t lw[4] = {lo[i].x, lo[i].y, lo[i].z, lo[i].w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float2 h2 = unpack_f16(hw[j]), l2 = unpack_f16(lw[j]);
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                  const int e = 8 * i + 2 * j + b;
-                  float cf = coef;
-                  if (p.use_diag && p.tall) cf += __ldcg(diag + min(col + e, p.side - 1));
-                  const float x = fmaf(b ? l2.y : l2.x, 1.0f / kLoScale, b ? h2.y : h2.x);
-                  y[e] = fmaf(cf, x, __uint_as_float(v[e]));
-                }
-              }
-            }
-            if (!p.last) {
-              staging_free();
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint32_t wh[4], wl[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const int e = 8 * i + 2 * j;
-                  wh[j] = pack_f16(y[e], y[e + 1]);
-                  const float2 h2 = unpack_f16(wh[j]);
-                  wl[j] = pack_f16((y[e] - h2.x) * kLoScale, (y[e + 1] - h2.y) * kLoScale);
-                }
-                put64(0, i, make_uint4(wh[0], wh[1], wh[2], wh[3]));
-                put64(1, i, make_uint4(wl[0], wl[1], wl[2], wl[3]));
-              }
-              staged();
-              store(&tm_d, 0, 64, t.m0, limit, col, 0, t.z, false, false);
-              store(&tm_d2, 2048, 64, t.m0, limit, col, 0, t.z, false, false);
-            } else if (p.direct) {
-              __nv_bfloat16* dst =
-                  p.out + (static_cast<int64_t>(t.z) * p.m_total + t.m0 + r) * p.n_total + col;
-              if (mine) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (col + e < p.n_total) dst[e] = __float2bfloat16_rn(y[e] * p.beta);
-              }
-            } else {
-              staging_free();
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint32_t w[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  w[j] = pack_b16(y[8 * i + 2 * j] * p.beta, y[8 * i + 2 * j + 1] * p.beta);
-                put64(0, i, make_uint4(w[0], w[1], w[2], w[3]));
-              }
-              staged();
-              store(&tm_d, 0, 64, t.m0, limit, col, 0, t.z, false, false);
             }
           }
         } else if (kEpi == Epi::Weights && p.out_f32) {
 #pragma unroll 1
-          for (int c = 0; c < TN / 64; ++c) {
-            const int col = t.n0 + hf * (TN / 2) + 32 * c;
+          for (int c = 0; c < kHalfCols / 32; ++c) {
+            const int col = col0 + 32 * c;
             if (col >= p.n_total) break;
             uint32_t v[32];
-            if (t.nk > 0) {
-              tmem_ld32(tacc + hf * (TN / 2) + 32 * c, v);
-              tmem_ld_wait();
-            } else {
+            acc32(hf * kHalfCols + 32 * c, v);
+            buffer_free();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = 0;
-            }
-            staging_free();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) put128(i, make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
-            staged();
-            store(&tm_d, 0, 128, t.m0, limit, col, 0, t.z, false, p.accumulate != 0);
+            for (int i = 0; i < 8; ++i) put(at128(i), v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            stored([&] { store(&tm_d, 0, 128, col, t.z, false); });
           }
-        } else {  // Rows, Weights in bf16, Gram, Poly: 64 columns at a time
-          const __half* c_row = nullptr;
-          if (kEpi == Epi::Poly) c_row = p.c0 + t.z * p.zc + (static_cast<int64_t>(t.m0) + r) * p.ldc;
+        } else if (kEpi == Epi::Gram) {
 #pragma unroll 1
-          for (int c = 0; c < TN / 128; ++c) {
-            const int col = t.n0 + hf * (TN / 2) + 64 * c;
+          for (int c = 0; c < kHalfCols / 32; ++c) {
+            const int col = col0 + 32 * c;
+            if (col >= p.n_total) break;
+            uint32_t v[32], w[16];
+            acc32(hf * kHalfCols + 32 * c, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              w[i] = pack_f16(p.alpha * __uint_as_float(v[2 * i]), p.alpha * __uint_as_float(v[2 * i + 1]));
+            buffer_free();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) put(at64(0, i), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            if (t.mirror) put_transposed(w);
+            stored([&] {
+              store(&tm_d, 0, 64, col, t.z, false);
+              if (t.mirror) tma_store_3d(&tm_d, buffer() + 2048, t.m0 + 32 * q, col, t.z);
+            });
+          }
+        } else {  // Rows, Weights in bf16: 64 columns at a time
+#pragma unroll 1
+          for (int c = 0; c < kHalfCols / 64; ++c) {
+            const int col = col0 + 64 * c;
             if (col >= p.n_total) break;
             uint32_t w[32];
 #pragma unroll
             for (int s2 = 0; s2 < 2; ++s2) {
               uint32_t v[32];
-              if (kSched != Sched::Experts || t.nk > 0) {
-                tmem_ld32(tacc + hf * (TN / 2) + 64 * c + 32 * s2, v);
-                tmem_ld_wait();
-              } else {
+              acc32(hf * kHalfCols + 64 * c + 32 * s2, v);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = 0;
-              }
-              if (kEpi == Epi::Poly) {
-                uint4 g[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  g[i] = make_uint4(0, 0, 0, 0);
-                  if (mine && col + 32 * s2 + 8 * i < p.n_total)
-                    g[i] = __ldcg(reinterpret_cast<const uint4*>(c_row + col + 32 * s2) + i);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const uint32_t gw[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) {
-                    const float2 g2 = unpack_f16(gw[j]);
-                    float o[2];
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                      const int e = 8 * i + 2 * j + b;
-                      o[b] = fmaf(p.beta, b ? g2.y : g2.x, p.alpha * __uint_as_float(v[e]));
-                      if (p.use_diag && col + 32 * s2 + e == t.m0 + r && mine) {
-                        p.diag[static_cast<int64_t>(t.z) * p.side + t.m0 + r] = o[b];
-                        o[b] = 0.f;
-                      }
-                    }
-                    w[16 * s2 + 4 * i + j] = pack_f16(o[0], o[1]);
-                  }
-                }
-              } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const float a = __uint_as_float(v[2 * i]), b = __uint_as_float(v[2 * i + 1]);
-                  w[16 * s2 + i] = kEpi == Epi::Gram ? pack_f16(p.alpha * a, p.alpha * b) : mine ? pack_b16(a, b) : 0u;
-                }
+              for (int i = 0; i < 16; ++i) {
+                const float x = __uint_as_float(v[2 * i]), y = __uint_as_float(v[2 * i + 1]);
+                w[16 * s2 + i] = mine ? pack_b16(x, y) : 0u;
               }
             }
-            staging_free();
+            buffer_free();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) put128(i, make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
-            staged();
-            store(&tm_d, 0, 128, t.m0, limit, col, 0, kSched == Sched::Blocks ? 0 : t.z, false, false);
+            for (int i = 0; i < 8; ++i) put(at128(i), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            stored([&] { store(&tm_d, 0, 128, col, kSched == Sched::Blocks ? 0 : t.z, false); });
           }
         }
+        if (!ok) break;
       }
       if (t.nk > 0) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_empty[buf]);
+        if (lane == 0) {
+          if (kPair)
+            mbar_arrive_cluster(cluster_addr(&acc_empty[buf], 0));
+          else
+            mbar_arrive(&acc_empty[buf]);
+        }
         ++acc_it;
       }
     }
     if (lane == 0) bulk_wait_all();
   }
 
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (*abort_flag) {
@@ -680,16 +832,20 @@ __global__ void __launch_bounds__(kGThreads, 1)
     const unsigned long long t0 = globaltimer();
     while (globaltimer() - t0 < 100000ull) __nanosleep(1000);
   }
+  __syncwarp();
+  if (kPair) cluster_sync();  // neither CTA leaves while the other may still read or signal it
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tbase, kTmemCols);
+    if (kPair)
+      tmem_dealloc_pair(tbase, kTmemCols);
+    else
+      tmem_dealloc(tbase, kTmemCols);
   }
 }
 
 // ------------------------------------------------------------------ host side
 // 3-D tensor map over 16-bit (or fp32) elements: dims d0 (contiguous), d1, d2
-// with strides s1, s2 in bytes, box b0 x b1 x 1 or, for row_last, b0 x 1 x b1.
-// row_bytes of the box: 128 or 64, which also names the swizzle.
+// with strides s1, s2 in bytes.  A box row of 128 or 64 bytes names the swizzle.
 enum class Elem { Bf16, F16, F32 };
 inline int make_map3(CUtensorMap* m, const void* base, Elem el, int64_t d0, int64_t d1, int64_t d2, int64_t s1,
                      int64_t s2, int b0, int b1, int b2) {
@@ -710,33 +866,46 @@ inline int make_map3(CUtensorMap* m, const void* base, Elem el, int64_t d0, int6
   return MOE_OK;
 }
 
-// Launches one product; pdl: chained to the launch before it.
-template <Form kForm, Sched kSched, Epi kEpi, int TN, bool kBf16>
-int launch_tile_gemm(const char* nm, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& d,
-                     const CUtensorMap& d2, const GemmParams& p, int64_t max_units, bool pdl, cudaStream_t stream) {
-  auto kernel = tile_gemm_kernel<kForm, kSched, kEpi, TN, kBf16>;
-  constexpr int smem = GemmShape<TN>::smem;
+struct GemmMaps {
+  CUtensorMap a, b, d, d2, c, c2;
+};
+
+// Launches one product of at most max_tiles tiles; pdl: chained to the launch before it.
+template <Form kForm, Sched kSched, Epi kEpi, bool kPair, bool kBf16>
+int launch_tile_gemm(const char* nm, const GemmMaps& m, const GemmParams& p, int64_t max_tiles, bool pdl,
+                     cudaStream_t stream) {
+  auto kernel = tile_gemm_kernel<kForm, kSched, kEpi, kPair, kBf16>;
   static std::atomic<bool> attr_set[kMaxDevices];  // per device; setting it twice is harmless
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cuda_fail("cudaGetDevice");
   if (dev >= kMaxDevices || !attr_set[dev].load(std::memory_order_relaxed)) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem);
     if (e != cudaSuccess) return cuda_fail(nm, e);
     if (dev < kMaxDevices) attr_set[dev].store(true, std::memory_order_relaxed);
   }
   const int nsm = sm_count();
   if (nsm <= 0) return cuda_fail("cudaDeviceGetAttribute(SM count)");
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  const int64_t slots = kPair ? nsm / 2 : nsm;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (kPair) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = 2;
+    attr[n].val.clusterDim.y = 1;
+    attr[n++].val.clusterDim.z = 1;
+  }
+  if (pdl) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
   cudaLaunchConfig_t c = {};
-  c.gridDim = dim3(static_cast<unsigned>(max_units < nsm ? max_units : nsm), 1, 1);
+  c.gridDim = dim3(static_cast<unsigned>((max_tiles < slots ? max_tiles : slots) * (kPair ? 2 : 1)), 1, 1);
   c.blockDim = dim3(kGThreads, 1, 1);
-  c.dynamicSmemBytes = smem;
+  c.dynamicSmemBytes = kGSmem;
   c.stream = stream;
   c.attrs = attr;
-  c.numAttrs = pdl ? 1 : 0;
-  const cudaError_t err = cudaLaunchKernelEx(&c, kernel, a, b, d, d2, p);
+  c.numAttrs = n;
+  const cudaError_t err = cudaLaunchKernelEx(&c, kernel, m.a, m.b, m.d, m.d2, m.c, m.c2, p);
   return err == cudaSuccess ? MOE_OK : cuda_fail(nm, err);
 }
 

@@ -103,6 +103,8 @@ SHAPES = [
     (1000, 8, 24, 128, 264, 1040),
     (77, 1, 200, 16, 136, 48),         # most experts empty
     (2000, 2, 2, 16, 72, 80),          # very many small blocks
+    (3000, 4, 24, 16, 520, 1040),      # tiles enough for every pair of SMs, tails in every direction
+    (2100, 3, 20, 128, 456, 528),
 ]
 
 

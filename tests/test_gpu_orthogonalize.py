@@ -76,6 +76,16 @@ def test_larger_matrices():
         check(moe.moe_orthogonalize(g), reference(g))
 
 
+@pytest.mark.parametrize("E,M,N", [(80, 100, 300), (75, 300, 72), (20, 520, 700), (19, 777, 513)])
+def test_many_matrices(E, M, N):
+    """Enough tiles for every pair of SMs, with tails on both sides."""
+    import mixture_experts_ffn_planner_b200 as moe
+
+    g = matrices(E, M, N, "lowrank", "bfloat16")
+    check(moe.moe_orthogonalize(g), reference(g))
+    moe.moe_device_status()
+
+
 @pytest.mark.parametrize("M,N", [(40, 96), (96, 40), (200, 136), (136, 200)])
 def test_steps_coefficients_and_eps(M, N):
     import mixture_experts_ffn_planner_b200 as moe
