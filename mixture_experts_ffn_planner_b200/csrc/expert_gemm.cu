@@ -113,7 +113,8 @@ static int blocks_tiled(const ExpertCall& c, const void* in, int64_t width_in, c
   p.nk = static_cast<int>(ceil_div(width_in, kGK));
   p.store_rows = std::min(c.bm, 32);
   GemmMaps m;
-  int rc = rows_map(&m.a, c, in, width_in, kGK, 128);
+  p.a_rows = kPair ? 128 : 32;
+  int rc = rows_map(&m.a, c, in, width_in, kGK, p.a_rows);
   if (rc == MOE_OK) {
     if (kForm == Form::NN)
       rc = weights_map(&m.b, w, Elem::Bf16, w_cols, w_rows, c.E, 64, kGK);
@@ -124,7 +125,7 @@ static int blocks_tiled(const ExpertCall& c, const void* in, int64_t width_in, c
   }
   if (rc == MOE_OK) {
     if (kEpi == Epi::Rows)
-      rc = rows_map(&m.d, c, out, width_out, 64, p.store_rows);
+      rc = rows_map(&m.d, c, out, width_out, 32, p.store_rows);
     else
       rc = halves_map(&m.d, c, out, width_out, 32, p.store_rows);
   }
@@ -165,7 +166,7 @@ static int weights_tiled(const ExpertCall& c, const void* a, int64_t m, const vo
   one.capacity = std::max<int64_t>(c.capacity, 1);
   int rc = rows_map(&t.a, one, c.capacity ? a : grad, m, 64, kGK);
   if (rc == MOE_OK) rc = rows_map(&t.b, one, c.capacity ? b : grad, n, 64, kGK);
-  if (rc == MOE_OK) rc = weights_map(&t.d, grad, f32 ? Elem::F32 : Elem::Bf16, n, m, c.E, f32 ? 32 : 64, 32);
+  if (rc == MOE_OK) rc = weights_map(&t.d, grad, f32 ? Elem::F32 : Elem::Bf16, n, m, c.E, f32 ? 16 : 32, 32);
   if (rc != MOE_OK) return rc;
   t.d2 = t.c = t.c2 = t.d;
   return launch_tile_gemm<Form::TN, Sched::Experts, Epi::Weights, kPair, true>(

@@ -428,6 +428,7 @@ static int ns_steps(const NsCall& n) {
   if ((rc = status_word(n.nm, &base.status)) != MOE_OK) return rc;
   base.wait_ns = kWaitTimeoutNs;
   base.batches = n.E;
+  base.a_rows = 128;
   base.store_rows = 32;
   base.side = S;
   base.diag = reinterpret_cast<float*>(n.ws + L.diag);

@@ -29,6 +29,20 @@ __device__ __forceinline__ uint32_t lane_id() {
   return l;
 }
 
+// True in one lane of the (converged) warp.  What an instruction takes from
+// uniform registers (TMA copies, MMAs) is then computed by the whole warp and
+// only the instruction itself predicated, where behind `lane == 0` every
+// operand is moved over one by one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t pred;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(pred));
+  return pred != 0;
+}
+
 // ----------------------------------------------------------------- cluster
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;
@@ -110,12 +124,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
                                           int* status, unsigned long long limit_ns) {
   auto done = [&] { return kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
   if (done()) return true;
-  const unsigned long long t0 = globaltimer();
-  // the timer is read every 16 polls, or on every poll under a short (test) limit
+  // the timer is read from the 16th poll on and then every 16 polls, or on every poll under a short (test) limit
   const uint32_t mask = limit_ns < 1000000ull ? 0u : 15u;
+  unsigned long long t0 = 0;
   for (uint32_t it = 1;; ++it) {
     if (done()) return true;
     if ((it & mask) == 0) {
+      if (t0 == 0) t0 = globaltimer();
       if (*abort_flag) return false;
       if (globaltimer() - t0 > limit_ns) {
         *abort_flag = 1;
@@ -278,6 +293,26 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// mma_f16 and tc_commit executed by a converged warp, one lane of it issuing:
+// without a branch the operands stay in uniform registers.
+__device__ __forceinline__ void mma_f16_one(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit_one(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
       : "memory");
 }
 

@@ -18,11 +18,12 @@
 // weights' bytes bound the call and 148 CTAs stream more of them at once.
 //
 // One CTA per SM walks the tiles.  Warp 0 copies operand chunks by TMA into a
-// ring of 5 stages, warp 1 (of the even CTA of a pair) issues the MMAs, one
+// ring of 5 or 6 stages (up, 8192 tokens on 64 experts: 543 us with 3, 485 with
+// 4, 471 with 5), warp 1 (of the even CTA of a pair) issues the MMAs, one
 // lane; warps 2-9 take a finished accumulator out of TMEM (two of them
 // alternate, so the epilogue of a tile runs beside the next tile's MMAs) and
-// store it by TMA from two swizzled staging buffers of 4 KB a warp.  What an
-// epilogue reads beside the accumulator (h, the iterate, the Gram matrix) is
+// store it by TMA from two swizzled staging buffers a warp, 32 columns of bf16
+// at a time.  What an epilogue reads beside the accumulator (h, the iterate, the Gram matrix) is
 // loaded by TMA into the staging buffer that its result then replaces, one
 // piece ahead: read by each thread from its own row, as the accumulator lies,
 // those loads took longer than the product.  Every wait is bounded.
@@ -31,7 +32,9 @@
 //   Blocks   rows of one expert (consecutive planner blocks, whatever block_m
 //            is) by columns of that expert's weights;
 //   Experts  a part of one expert's weight gradient, contracted over the
-//            expert's rows; what lies behind the last routed one in a chunk is
+//            expert's rows (where they begin is looked up once, into shared
+//            memory: searched for by every role at every tile, it made tiles of
+//            few rows cost 5.8 us); what lies behind the last routed one in a chunk is
 //            cleared in shared memory by warp 10, whatever it holds;
 //   Batch    a part of one matrix of a batch; of a symmetric one (Gram, Poly)
 //            the tiles on and above the diagonal, each stored as it is and
@@ -62,15 +65,22 @@ constexpr int kGK = 64;     // contraction indices a chunk
 constexpr int kGRow = 128;  // bytes of an operand row in a stage
 constexpr int kGHalf = 128 * kGRow;   // bytes of a CTA's A, and of its B, a chunk
 constexpr int kGStage = 2 * kGHalf;
-constexpr int kGStages = 5;
 constexpr int kGEpiWarps = 8;
 constexpr int kGPatchWarp = 2 + kGEpiWarps;
 constexpr int kGThreads = 32 * (3 + kGEpiWarps);
-constexpr int kGBuf = 4096;  // bytes of a staging buffer; two a warp
-constexpr int kGStaging = kGStages * kGStage;
-constexpr int kGCtrl = kGStaging + kGEpiWarps * 2 * kGBuf;
-constexpr int kGSmem = 1024 + kGCtrl + 512;
-static_assert(kGSmem <= 232448, "shared memory");
+constexpr int kGTile = 32 * 64;  // bytes of a staging tile: 32 rows of 64
+// epilogues that read a second operand
+constexpr bool epi_side(Epi e) { return e == Epi::SwigluGrad || e == Epi::Poly || e == Epi::Update; }
+constexpr int gemm_stages(Sched s, Epi e) { return epi_side(e) || s == Sched::Experts ? 5 : 6; }
+constexpr int gemm_buf(Epi e) { return (epi_side(e) ? 2 : 1) * kGTile; }  // bytes of a staging buffer; two a warp
+constexpr int gemm_ctrl(Sched s, Epi e) { return gemm_stages(s, e) * kGStage + kGEpiWarps * 2 * gemm_buf(e); }
+constexpr int kGCtrlBytes = 512;
+constexpr int gemm_smem(Sched s, Epi e) {
+  return 1024 + gemm_ctrl(s, e) + kGCtrlBytes + (s == Sched::Experts ? 4 * (kMaxExperts + 1) : 0);
+}
+static_assert(gemm_smem(Sched::Blocks, Epi::Rows) <= 232448 && gemm_smem(Sched::Batch, Epi::Update) <= 232448 &&
+                  gemm_smem(Sched::Experts, Epi::Weights) <= 232448,
+              "shared memory");
 constexpr float kLoScale = 2048.0f;  // lo = fp16(2048 * (value - hi)): 11 more bits
 
 constexpr int tile_m(bool pair) { return pair ? 256 : 128; }
@@ -86,6 +96,7 @@ struct GemmParams {
   int m_tiles, n_tiles, batches;
   int m_total, n_total;  // rows (Experts, Batch) and columns of D; GateUp, SwigluGrad: columns of act
   int nk;                // chunks of the contraction (Blocks, Batch)
+  int a_rows;            // rows of A's boxes (A K-major): 128, or 32 where tiles have few rows
   int store_rows;        // rows of the store (and side) boxes
   // Weights
   int out_f32, accumulate;
@@ -117,25 +128,22 @@ __device__ __forceinline__ float2 unpack_f16(uint32_t w) {
 struct Tile {
   int z;       // expert or matrix
   int m0, n0;  // this CTA's first row of A, the tile's first column
-  int limit;   // rows of this CTA's half that belong to the output (<= 0: none)
+  int total;   // rows of the tile that belong to the output
+  int limit;   // those of this CTA's half (<= 0: none)
   int nk;      // chunks; 0: a weight gradient without rows
   bool mirror; // symmetric: the transposed tile is stored too
   int p0;      // Experts: first row of the contraction
   int rows;    // Experts: its routed rows
 };
 
-// First of the n ascending ids that is >= e (warp-collective; 32 probes a round).
-__device__ __forceinline__ int warp_lower_bound(const int32_t* ids, int n, int e, int lane) {
-  int lo = 0, hi = n;
-  while (lo < hi) {
-    const int step = (hi - lo + 31) / 32;
-    const int i = lo + lane * step;
-    const int below = __popc(__ballot_sync(0xffffffffu, lane * step < hi - lo && __ldg(ids + min(i, n - 1)) < e));
-    if (below == 0) break;
-    hi = min(hi, lo + below * step);
-    lo += (below - 1) * step + 1;
+// first[e], e <= E: the first of the plan's blocks whose expert is >= e (by all threads; the ids ascend, and
+// what does not stays in range).
+__device__ __forceinline__ void find_segments(const GemmParams& p, int blocks, int* first) {
+  for (int b = static_cast<int>(threadIdx.x); b <= blocks; b += kGThreads) {
+    const int lo = b == 0 ? 0 : min(max(__ldg(p.expert_ids + b - 1), 0), p.E) + 1;
+    const int hi = b == blocks ? p.E : min(__ldg(p.expert_ids + b), p.E);
+    for (int e = lo; e <= hi; ++e) first[e] = b;
   }
-  return lo;
 }
 
 // The tiles of one role, in the order that every role walks them: tile numbers
@@ -146,24 +154,36 @@ struct Walk {
   static constexpr bool kSym = kEpi == Epi::Gram || kEpi == Epi::Poly;  // square tiles, m_tiles == n_tiles
   const GemmParams& p;
   const int lane, rank, stride;
-  int u, blocks, units, per_z;
+  const int blocks;
+  int u, units, per_z;
   // Blocks: a window of 32 blocks and those in it that begin a tile of their expert
   int win = 0, before = 0, carry = 0, prev = -1, id = -1;
   uint32_t heads = 0;
-  // Experts
-  int z_seen = -1, seg_lo = 0, seg_rows = 0;
+  // Experts: the segments, and the order's ids in the last block of the next tile's expert, 32 an element
+  const int* first;
+  int z_next = -1;
+  int last_ids[4];
 
-  __device__ __forceinline__ Walk(const GemmParams& p_, int rank_)
-      : p(p_), lane(static_cast<int>(lane_id())), rank(rank_), stride(kPair ? gridDim.x / 2 : gridDim.x) {
+  __device__ __forceinline__ Walk(const GemmParams& p_, int rank_, int blocks_, const int* first_)
+      : p(p_), lane(static_cast<int>(lane_id())), rank(rank_), stride(kPair ? gridDim.x / 2 : gridDim.x), blocks(blocks_),
+        first(first_) {
     u = kPair ? blockIdx.x / 2 : blockIdx.x;
-    blocks = 0;
-    if (kSched != Sched::Batch) {
-      const int n = __ldg(p.ntpp) / p.bm;
-      blocks = n < 0 ? 0 : min(n, p.max_blocks);
-    }
     per_z = kSym ? p.m_tiles * (p.m_tiles + 1) / 2 : p.m_tiles * p.n_tiles;
     units = p.batches * per_z;
     if (kSched == Sched::Blocks) look(0);
+    if (kSched == Sched::Experts) peek();
+  }
+
+  // Starts the loads of last_ids for tile u, a tile ahead of their use.
+  __device__ __forceinline__ void peek() {
+    if (u >= units || u / per_z == z_next) return;
+    z_next = u / per_z;
+    const int end = first[z_next + 1];
+    const bool any = first[z_next] < end;
+    const int64_t at = static_cast<int64_t>(end - 1) * p.bm;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      last_ids[i] = any && 32 * i + lane < p.bm ? __ldg(p.sorted_ids + at + 32 * i + lane) : -1;
   }
 
   // The window from block `at` on: a tile begins every tile_m / bm blocks of an expert's run.
@@ -198,7 +218,8 @@ struct Walk {
           0xffffffffu, lane < per && b + lane < blocks && __ldg(p.expert_ids + min(b + lane, blocks - 1)) == t->z);
       const int run = same == 0xffffffffu ? 32 : __ffs(static_cast<int>(~same)) - 1;
       t->m0 = b * p.bm + rank * 128;
-      t->limit = min(128, run * p.bm - rank * 128);
+      t->total = run * p.bm;
+      t->limit = min(128, t->total - rank * 128);
       t->nk = p.nk;
       t->p0 = t->rows = 0;
       t->mirror = false;
@@ -219,26 +240,22 @@ struct Walk {
     }
     t->m0 = mi * tile_m(kPair) + rank * 128;
     t->n0 = ni * kCols;
+    t->total = p.m_total - mi * tile_m(kPair);
     t->limit = min(128, p.m_total - t->m0);
     t->nk = p.nk;
     t->p0 = t->rows = 0;
     if (kSched == Sched::Experts) {
-      if (t->z != z_seen) {  // warp-uniform
-        z_seen = t->z;
-        seg_lo = warp_lower_bound(p.expert_ids, blocks, t->z, lane);
-        const int n = warp_lower_bound(p.expert_ids + seg_lo, blocks - seg_lo, t->z + 1, lane);
-        seg_rows = 0;
-        if (n > 0) {  // whole blocks, and the routed rows that the last one begins with
-          const int64_t at = static_cast<int64_t>(seg_lo + n - 1) * p.bm;
-          int last = 0;
-          for (int q = 0; q < p.bm; q += 32)
-            last += __popc(__ballot_sync(0xffffffffu, q + lane < p.bm && __ldg(p.sorted_ids + at + min(q + lane, p.bm - 1)) >= 0));
-          seg_rows = (n - 1) * p.bm + last;
-        }
+      const int lo = first[t->z], n = first[t->z + 1] - lo;
+      t->p0 = lo * p.bm;
+      if (n > 0) {  // whole blocks, and the routed rows that the last one begins with
+        t->rows = (n - 1) * p.bm;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t->rows += __popc(__ballot_sync(0xffffffffu, last_ids[i] >= 0));
       }
-      t->p0 = seg_lo * p.bm;
-      t->rows = seg_rows;
-      t->nk = (seg_rows + kGK - 1) / kGK;
+      t->nk = (t->rows + kGK - 1) / kGK;
+      u += stride;
+      peek();
+      return true;
     }
     u += stride;
     return true;
@@ -258,20 +275,24 @@ __global__ void __launch_bounds__(kGThreads, 1)
   constexpr int kN = tile_n(kPair);
   constexpr uint32_t kTmemCols = 2 * kN;
   constexpr bool kAMn = kForm == Form::TN, kBMn = kForm != Form::NT;
-  // epilogues that read a second operand (side tiles of 32 columns; one or two at once)
-  constexpr bool kSide = kEpi == Epi::SwigluGrad || kEpi == Epi::Poly || kEpi == Epi::Update;
+  constexpr int kStages = gemm_stages(kSched, kEpi), kBuf = gemm_buf(kEpi);
+  constexpr int kStaging = kStages * kGStage, kCtrl = gemm_ctrl(kSched, kEpi);
+  // side tiles of 32 columns, one or two at once
+  constexpr bool kSide = epi_side(kEpi);
   constexpr int kSideTiles = kEpi == Epi::Poly ? 1 : 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kGCtrl);
-  uint64_t* empty = full + kGStages;
-  uint64_t* part = empty + kGStages;      // ragged chunks: landed, not yet cleared
-  uint64_t* acc_full = part + kGStages;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kCtrl);
+  uint64_t* empty = full + kStages;
+  uint64_t* part = empty + kStages;      // ragged chunks: landed, not yet cleared
+  uint64_t* acc_full = part + kStages;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* side_full = acc_empty + 2;    // [kGEpiWarps][2]
   uint32_t* tmem_base_sm = reinterpret_cast<uint32_t*>(side_full + 2 * kGEpiWarps);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_sm + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int* first = reinterpret_cast<int*>(smem + kCtrl + kGCtrlBytes);
+  // by shuffle, so that the compiler knows them to be the same in all lanes, and the roles' operands to be uniform
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = kPair ? cluster_ctarank() : 0u;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return mbar_wait(bar, parity, abort_flag, p.status, p.wait_ns);
@@ -284,7 +305,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
 
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kGStages; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       // pair: the even CTA's twice, for the copies of both, or warp 10 of each
       mbar_init(&full[s], kPair ? 2 : 1);
       mbar_init(&empty[s], 1);
@@ -311,13 +332,19 @@ __global__ void __launch_bounds__(kGThreads, 1)
       tmem_relinquish();
     }
   }
+  int blocks = 0;
+  if (kSched != Sched::Batch) {  // the plan; these launches are not chained
+    const int n = __ldg(p.ntpp) / p.bm;
+    blocks = n < 0 ? 0 : min(n, p.max_blocks);
+    if (kSched == Sched::Experts) find_segments(p, blocks, first);
+  }
   tc_fence_before();
   __syncthreads();
   if (kPair) cluster_sync();  // the other CTA's barriers are ready
   tc_fence_after();
-  const uint32_t tbase = *tmem_base_sm;
-  pdl_wait();  // what a chained launch before this one wrote is read below
-  Walk<kSched, kEpi, kPair> walk(p, static_cast<int>(rank));
+  const uint32_t tbase = __shfl_sync(0xffffffffu, *tmem_base_sm, 0);
+  if (kSched == Sched::Batch) pdl_wait();  // what a chained launch before this one wrote is read below
+  Walk<kSched, kEpi, kPair> walk(p, static_cast<int>(rank), blocks, first);
   Tile t;
 
   if (warp == 0) {
@@ -330,51 +357,53 @@ __global__ void __launch_bounds__(kGThreads, 1)
       const int za = kSched == Sched::Batch ? t.z : 0;
       const int zb = kSched == Sched::Experts ? 0 : t.z;
       const int r = static_cast<int>(rank);
+      // rows behind the tile's last are not loaded: what is in shared memory there reaches no row that is stored
+      const int boxes = kAMn ? 0 : t.limit > 0 ? (t.limit + p.a_rows - 1) / p.a_rows : 0;
+      const uint32_t mine = kGHalf + (kAMn ? kGHalf : boxes * p.a_rows * kGRow);
+      const uint32_t bytes = !kPair ? mine : 2 * kGHalf + (kAMn || t.total > 128 ? 2 * kGHalf : kGHalf);
       for (int kc = 0; kc < t.nk; ++kc) {
-        if (lane == 0) {
-          ok = wait(&empty[s], ph ^ 1u);
-          if (ok) {
-            uint8_t* a = smem + s * kGStage;
-            uint8_t* b = a + kGHalf;
-            const int k0 = t.p0 + kc * kGK;
-            const bool held = kSched == Sched::Experts && ragged(t, kc);
-            const uint32_t bar = held || !kPair ? smem_u32(held ? &part[s] : &full[s]) : cluster_addr(&full[s], 0);
-            if (held) {
-              mbar_arrive_expect_tx(&part[s], kGStage);
-            } else if (rank == 0) {  // the odd CTA's copies complete on the even one's barrier
-              mbar_arrive_expect_tx(&full[s], kPair ? 2 * kGStage : kGStage);
-              if (kPair) mbar_arrive(&full[s]);
-            }
-            auto load = [&](void* dst, const CUtensorMap* map, int c0, int c1, int c2) {
-              if (kPair)
-                tma_load_3d_pair(dst, map, bar, c0, c1, c2, pol);
-              else
-                tma_load_3d(dst, map, held ? &part[s] : &full[s], c0, c1, c2, pol);
-            };
-            if (kAMn) {
-              load(a, &tm_a, t.m0, k0, za);
-              load(a + kGHalf / 2, &tm_a, t.m0 + 64, k0, za);
+        ok = __all_sync(0xffffffffu, wait(&empty[s], ph ^ 1u));
+        if (!ok) break;
+        uint8_t* a = smem + s * kGStage;
+        uint8_t* b = a + kGHalf;
+        const int k0 = t.p0 + kc * kGK;
+        const bool held = kSched == Sched::Experts && ragged(t, kc);
+        const uint32_t bar = held || !kPair ? smem_u32(held ? &part[s] : &full[s]) : cluster_addr(&full[s], 0);
+        if (elect_one()) {
+          if (held) {
+            mbar_arrive_expect_tx(&part[s], mine);
+          } else if (rank == 0) {  // the odd CTA's copies complete on the even one's barrier
+            mbar_arrive_expect_tx(&full[s], bytes);
+            if (kPair) mbar_arrive(&full[s]);
+          }
+          auto load = [&](void* dst, const CUtensorMap* map, int c0, int c1, int c2) {
+            if (kPair)
+              tma_load_3d_pair(dst, map, bar, c0, c1, c2, pol);
+            else
+              tma_load_3d(dst, map, held ? &part[s] : &full[s], c0, c1, c2, pol);
+          };
+          if (kAMn) {
+            load(a, &tm_a, t.m0, k0, za);
+            load(a + kGHalf / 2, &tm_a, t.m0 + 64, k0, za);
+          } else {
+            for (int i = 0; i < boxes; ++i) load(a + i * p.a_rows * kGRow, &tm_a, k0, t.m0 + i * p.a_rows, za);
+          }
+          if (kBMn) {
+            load(b, &tm_b, t.n0 + 128 * r, k0, zb);
+            load(b + kGHalf / 2, &tm_b, t.n0 + 128 * r + 64, k0, zb);
+          } else if (kEpi == Epi::GateUp) {
+            if (kPair) {  // the even CTA holds the gate columns, the odd one the up columns
+              load(b, &tm_b, k0, t.n0, 2 * zb + r);
             } else {
-              load(a, &tm_a, k0, t.m0, za);
+              load(b, &tm_b, k0, t.n0, 2 * zb);
+              load(b + kGHalf / 2, &tm_b, k0, t.n0, 2 * zb + 1);
             }
-            if (kBMn) {
-              load(b, &tm_b, t.n0 + 128 * r, k0, zb);
-              load(b + kGHalf / 2, &tm_b, t.n0 + 128 * r + 64, k0, zb);
-            } else if (kEpi == Epi::GateUp) {
-              if (kPair) {  // the even CTA holds the gate columns, the odd one the up columns
-                load(b, &tm_b, k0, t.n0, 2 * zb + r);
-              } else {
-                load(b, &tm_b, k0, t.n0, 2 * zb);
-                load(b + kGHalf / 2, &tm_b, k0, t.n0, 2 * zb + 1);
-              }
-            } else {
-              load(b, &tm_b, k0, t.n0 + 128 * r, zb);
-            }
+          } else {
+            load(b, &tm_b, k0, t.n0 + 128 * r, zb);
           }
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        if (++s == kGStages) { s = 0; ph ^= 1u; }
+        __syncwarp();
+        if (++s == kStages) { s = 0; ph ^= 1u; }
       }
     }
   } else if (warp == 1) {
@@ -383,50 +412,54 @@ __global__ void __launch_bounds__(kGThreads, 1)
     int s = 0, acc_it = 0;
     uint32_t ph = 0;
     bool ok = rank == 0;
-    while (ok && walk.next(&t)) {
-      if (t.nk == 0) continue;
+    bool more = ok && walk.next(&t);
+    while (more) {
+      const Tile now = t;
+      if (now.nk == 0) {
+        more = walk.next(&t);
+        continue;
+      }
       const int buf = acc_it & 1;
-      if (lane == 0) ok = wait_cluster(&acc_empty[buf], ((acc_it >> 1) & 1) ^ 1u);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+      ok = __all_sync(0xffffffffu, wait_cluster(&acc_empty[buf], ((acc_it >> 1) & 1) ^ 1u));
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tbase + static_cast<uint32_t>(buf) * kN;
-      for (int kc = 0; kc < t.nk; ++kc) {
-        if (lane == 0) {
-          ok = kSched == Sched::Experts && ragged(t, kc) ? wait_cluster(&full[s], ph) : wait(&full[s], ph);
-          if (ok) {
-            tc_fence_after();
-            const uint32_t a = smem_u32(smem + s * kGStage), b = a + kGHalf;
-            const uint64_t ad = kAMn ? sdesc_sw128_mn(a, kGHalf / 2) : sdesc_sw128(a);
-            const uint64_t bd = kBMn ? sdesc_sw128_mn(b, kGHalf / 2) : sdesc_sw128(b);
-            // whole steps without a routed row are left out
-            const int steps = kSched == Sched::Experts && ragged(t, kc) ? (t.rows - kc * kGK + 15) / 16 : kGK / 16;
-#pragma unroll
-            for (int kk = 0; kk < kGK / 16; ++kk) {
-              if (kSched == Sched::Experts && kk >= steps) break;
-              // 16 contraction indices: 32 bytes of a K-major row, 16 rows of an MN-major one
-              const uint64_t ak = ad + (kAMn ? 128u : 2u) * kk, bk = bd + (kBMn ? 128u : 2u) * kk;
-              if (kPair)
-                mma_f16_pair(d, ak, bk, kIdesc, (kc | kk) != 0);
-              else
-                mma_f16(d, ak, bk, kIdesc, (kc | kk) != 0);
-            }
-            if (kPair)
-              tc_commit_pair(&empty[s]);
-            else
-              tc_commit(&empty[s]);
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+      for (int kc = 0; kc < now.nk; ++kc) {
+        const bool cut = kSched == Sched::Experts && ragged(now, kc);
+        ok = __all_sync(0xffffffffu, cut ? wait_cluster(&full[s], ph) : wait(&full[s], ph));
         if (!ok) break;
-        if (++s == kGStages) { s = 0; ph ^= 1u; }
+        tc_fence_after();
+        const uint32_t a = smem_u32(smem + s * kGStage), b = a + kGHalf;
+        const uint64_t ad = kAMn ? sdesc_sw128_mn(a, kGHalf / 2) : sdesc_sw128(a);
+        const uint64_t bd = kBMn ? sdesc_sw128_mn(b, kGHalf / 2) : sdesc_sw128(b);
+        // whole steps without a routed row are left out
+        const int steps = cut ? (now.rows - kc * kGK + 15) / 16 : kGK / 16;
+        // 16 contraction indices: 32 bytes of a K-major row, 16 rows of an MN-major one.  A predicated issue is the
+        // faster one for single CTAs (a chunk of 128 x 128 in 232 cycles of this warp, behind a branch 344), but not
+        // for pairs, whose MMAs take longer than their issue (up, 8192 tokens on 64 experts: 454 us, 440 behind it).
+        constexpr uint32_t kStepA = kAMn ? 128 : 2, kStepB = kBMn ? 128 : 2;
+        if (kPair) {
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < kGK / 16; ++kk)
+              if (kSched != Sched::Experts || kk < steps)
+                mma_f16_pair(d, ad + kStepA * kk, bd + kStepB * kk, kIdesc, (kc | kk) != 0);
+            tc_commit_pair(&empty[s]);
+            if (kc + 1 == now.nk) tc_commit_pair(&acc_full[buf]);
+          }
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < kGK / 16; ++kk)
+            if (kSched != Sched::Experts || kk < steps)
+              mma_f16_one(d, ad + kStepA * kk, bd + kStepB * kk, kIdesc, (kc | kk) != 0);
+          tc_commit_one(&empty[s]);
+          if (kc + 1 == now.nk) tc_commit_one(&acc_full[buf]);
+        }
+        __syncwarp();
+        if (++s == kStages) { s = 0; ph ^= 1u; }
+        if (kc == 0) more = walk.next(&t);  // beside the MMAs
       }
-      if (ok && lane == 0) {
-        if (kPair)
-          tc_commit_pair(&acc_full[buf]);
-        else
-          tc_commit(&acc_full[buf]);
-      }
+      if (!ok) break;
       ++acc_it;
     }
   } else if (warp == kGPatchWarp) {
@@ -439,7 +472,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
       bool ok = true;
       while (ok && walk.next(&t)) {
         if (t.nk > 0 && ragged(t, t.nk - 1)) {
-          const int s = (count + t.nk - 1) % kGStages;
+          const int s = (count + t.nk - 1) % kStages;
           ok = wait(&part[s], (seen >> s) & 1u);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -471,14 +504,12 @@ __global__ void __launch_bounds__(kGThreads, 1)
     const int q = warp & 3, hf = (warp - 2) >> 2;
     const int r = 32 * q + lane;
     constexpr int kHalfCols = kN / 2;
-    const uint32_t stg0 = smem_u32(smem + kGStaging + (warp - 2) * 2 * kGBuf);
+    const uint32_t stg0 = smem_u32(smem + kStaging + (warp - 2) * 2 * kBuf);
     uint64_t* side = side_full + (warp - 2) * 2;
     int piece = 0;  // pieces so far; piece % 2 is the buffer
-    auto buffer = [&] { return stg0 + static_cast<uint32_t>(piece & 1) * kGBuf; };
-    // 16 bytes of this thread's row of a staging tile, swizzled as its tensor
-    // map says: 128-byte rows, or 64-byte rows (two tiles a buffer)
-    auto at128 = [&](int i) { return buffer() + lane * 128 + ((i ^ (lane & 7)) << 4); };
-    auto at64 = [&](int tile, int i) { return buffer() + tile * 2048 + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4); };
+    auto buffer = [&] { return stg0 + static_cast<uint32_t>(piece & 1) * kBuf; };
+    // 16 bytes of this thread's row of a staging tile, swizzled as its tensor map says
+    auto at64 = [&](int tile, int i) { return buffer() + tile * kGTile + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4); };
     auto put = [&](uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
       asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
     };
@@ -488,15 +519,15 @@ __global__ void __launch_bounds__(kGThreads, 1)
                    : "r"(at)
                    : "memory");
     };
-    // a 32 x 32 piece in fp16 (w: this row's pairs) into the buffer's second tile, transposed: lanes 2i and
+    // a 32 x 32 piece in fp16 (w: this row's pairs) into a tile of the buffer, transposed: lanes 2i and
     // 2i + 1 exchange halves and write a pair each, to rows 2j and 2j + 1, without bank conflicts
-    auto put_transposed = [&](const uint32_t (&w)[16]) {
+    auto put_transposed = [&](int tile, const uint32_t (&w)[16]) {
       const bool odd = lane & 1;
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         const uint32_t other = __shfl_xor_sync(0xffffffffu, w[j], 1);
         const uint32_t pair = odd ? __byte_perm(other, w[j], 0x7632) : __byte_perm(w[j], other, 0x5410);
-        const uint32_t at = buffer() + 2048 + (2 * j + (odd ? 1 : 0)) * 64 + (((lane >> 3) ^ (j & 3)) << 4) + ((lane >> 1) & 3) * 4;
+        const uint32_t at = buffer() + tile * kGTile + (2 * j + (odd ? 1 : 0)) * 64 + (((lane >> 3) ^ (j & 3)) << 4) + ((lane >> 1) & 3) * 4;
         asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(pair) : "memory");
       }
     };
@@ -506,10 +537,10 @@ __global__ void __launch_bounds__(kGThreads, 1)
       __syncwarp();
     };
     // a tile of the buffer to `map`: this warp's rows below the limit, boxes of store_rows
-    auto store = [&](const CUtensorMap* map, int off, int row_bytes, int c0, int c1, bool row_last) {
+    auto store = [&](const CUtensorMap* map, int tile, int c0, int c1, bool row_last) {
       for (int i = 0; i < 32; i += p.store_rows) {
         if (32 * q + i >= t.limit) break;
-        const uint32_t src = buffer() + off + i * row_bytes;
+        const uint32_t src = buffer() + tile * kGTile + i * 64;
         const int row = t.m0 + 32 * q + i;
         if (kEpi == Epi::Weights && p.accumulate)
           tma_add_3d(map, src, c0, row, c1);
@@ -539,13 +570,13 @@ __global__ void __launch_bounds__(kGThreads, 1)
         const uint64_t pol = policy_evict_normal();
         for (int i = 0; i < boxes; ++i) {
           const int row = t.m0 + 32 * q + i * p.store_rows;
-          uint8_t* dst = smem + kGStaging + (warp - 2) * 2 * kGBuf + b * kGBuf + i * p.store_rows * 64;
+          uint8_t* dst = smem + kStaging + (warp - 2) * 2 * kBuf + b * kBuf + i * p.store_rows * 64;
           if (kEpi == Epi::SwigluGrad) {
             tma_load_3d(dst, &tm_c, &side[b], col, 0, row, pol);
-            tma_load_3d(dst + 2048, &tm_c, &side[b], col, 1, row, pol);
+            tma_load_3d(dst + kGTile, &tm_c, &side[b], col, 1, row, pol);
           } else {
             tma_load_3d(dst, &tm_c, &side[b], col, row, t.z, pol);
-            if (kSideTiles == 2) tma_load_3d(dst + 2048, &tm_c2, &side[b], col, row, t.z, pol);
+            if (kSideTiles == 2) tma_load_3d(dst + kGTile, &tm_c2, &side[b], col, row, t.z, pol);
           }
         }
       }
@@ -588,23 +619,21 @@ __global__ void __launch_bounds__(kGThreads, 1)
             tmem_ld32(tacc + ac, g);
             tmem_ld32(tacc + kN / 2 + ac, up);
             tmem_ld_wait();
-            buffer_free();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t wg[4], wu[4];
+            for (int half = 0; half < 2; ++half) {
+              buffer_free();
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int e = 8 * i + 2 * j;
-                wg[j] = mine ? pack_b16(__uint_as_float(g[e]), __uint_as_float(g[e + 1])) : 0u;
-                wu[j] = mine ? pack_b16(__uint_as_float(up[e]), __uint_as_float(up[e + 1])) : 0u;
+              for (int i = 0; i < 4; ++i) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const int e = 8 * i + 2 * j;
+                  w[j] = mine ? pack_b16(__uint_as_float(half ? up[e] : g[e]), __uint_as_float(half ? up[e + 1] : g[e + 1])) : 0u;
+                }
+                put(at64(0, i), w[0], w[1], w[2], w[3]);
               }
-              put(at64(0, i), wg[0], wg[1], wg[2], wg[3]);
-              put(at64(1, i), wu[0], wu[1], wu[2], wu[3]);
+              stored([&] { store(&tm_d, 0, col, half, true); });
             }
-            stored([&] {
-              store(&tm_d, 0, 64, col, 0, true);
-              store(&tm_d, 2048, 64, col, 1, true);
-            });
             buffer_free();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -618,7 +647,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
               }
               put(at64(0, i), w[0], w[1], w[2], w[3]);
             }
-            stored([&] { store(&tm_d2, 0, 64, col, 0, false); });
+            stored([&] { store(&tm_d2, 0, col, 0, false); });
           }
         } else if (kSide) {
 #pragma unroll 1
@@ -659,8 +688,8 @@ __global__ void __launch_bounds__(kGThreads, 1)
                 put(at64(1, i), ou[0], ou[1], ou[2], ou[3]);
               }
               stored([&] {
-                store(&tm_d, 0, 64, col, 0, true);
-                store(&tm_d, 2048, 64, col, 1, true);
+                store(&tm_d, 0, col, 0, true);
+                store(&tm_d, 1, col, 1, true);
               });
             } else if (kEpi == Epi::Poly) {
               uint32_t w[16];
@@ -685,10 +714,10 @@ __global__ void __launch_bounds__(kGThreads, 1)
                 }
                 put(at64(0, i), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
               }
-              if (t.mirror) put_transposed(w);
+              if (t.mirror) put_transposed(1, w);
               stored([&] {
-                store(&tm_d, 0, 64, col, t.z, false);
-                if (t.mirror) tma_store_3d(&tm_d, buffer() + 2048, t.m0 + 32 * q, col, t.z);
+                store(&tm_d, 0, col, t.z, false);
+                if (t.mirror) tma_store_3d(&tm_d, buffer() + kGTile, t.m0 + 32 * q, col, t.z);
               });
             } else {
               const float* diag = p.diag + static_cast<int64_t>(t.z) * p.side;
@@ -731,7 +760,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
                     w[j] = pack_b16(y[8 * i + 2 * j] * p.beta, y[8 * i + 2 * j + 1] * p.beta);
                   put(at64(0, i), w[0], w[1], w[2], w[3]);
                 }
-                stored([&] { store(&tm_d, 0, 64, col, t.z, false); });
+                stored([&] { store(&tm_d, 0, col, t.z, false); });
               } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -747,8 +776,8 @@ __global__ void __launch_bounds__(kGThreads, 1)
                   put(at64(1, i), wl[0], wl[1], wl[2], wl[3]);
                 }
                 stored([&] {
-                  store(&tm_d, 0, 64, col, t.z, false);
-                  store(&tm_d2, 2048, 64, col, t.z, false);
+                  store(&tm_d, 0, col, t.z, false);
+                  store(&tm_d2, 1, col, t.z, false);
                 });
               }
             }
@@ -760,10 +789,17 @@ __global__ void __launch_bounds__(kGThreads, 1)
             if (col >= p.n_total) break;
             uint32_t v[32];
             acc32(hf * kHalfCols + 32 * c, v);
-            buffer_free();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) put(at128(i), v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-            stored([&] { store(&tm_d, 0, 128, col, t.z, false); });
+            for (int half = 0; half < 2; ++half) {  // 16 columns of fp32 a tile
+              if (col + 16 * half >= p.n_total) break;
+              buffer_free();
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int e = 16 * half + 4 * i;
+                put(at64(0, i), v[e], v[e + 1], v[e + 2], v[e + 3]);
+              }
+              stored([&] { store(&tm_d, 0, col + 16 * half, t.z, false); });
+            }
           }
         } else if (kEpi == Epi::Gram) {
 #pragma unroll 1
@@ -778,32 +814,32 @@ __global__ void __launch_bounds__(kGThreads, 1)
             buffer_free();
 #pragma unroll
             for (int i = 0; i < 4; ++i) put(at64(0, i), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-            if (t.mirror) put_transposed(w);
-            stored([&] {
-              store(&tm_d, 0, 64, col, t.z, false);
-              if (t.mirror) tma_store_3d(&tm_d, buffer() + 2048, t.m0 + 32 * q, col, t.z);
-            });
-          }
-        } else {  // Rows, Weights in bf16: 64 columns at a time
-#pragma unroll 1
-          for (int c = 0; c < kHalfCols / 64; ++c) {
-            const int col = col0 + 64 * c;
-            if (col >= p.n_total) break;
-            uint32_t w[32];
-#pragma unroll
-            for (int s2 = 0; s2 < 2; ++s2) {
-              uint32_t v[32];
-              acc32(hf * kHalfCols + 64 * c + 32 * s2, v);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float x = __uint_as_float(v[2 * i]), y = __uint_as_float(v[2 * i + 1]);
-                w[16 * s2 + i] = mine ? pack_b16(x, y) : 0u;
-              }
+            stored([&] { store(&tm_d, 0, col, t.z, false); });
+            if (t.mirror) {
+              buffer_free();
+              put_transposed(0, w);
+              stored([&] { tma_store_3d(&tm_d, buffer(), t.m0 + 32 * q, col, t.z); });
             }
+          }
+        } else {  // Rows, Weights in bf16
+#pragma unroll 1
+          for (int c = 0; c < kHalfCols / 32; ++c) {
+            const int col = col0 + 32 * c;
+            if (col >= p.n_total) break;
+            uint32_t v[32];
+            acc32(hf * kHalfCols + 32 * c, v);
             buffer_free();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) put(at128(i), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-            stored([&] { store(&tm_d, 0, 128, col, kSched == Sched::Blocks ? 0 : t.z, false); });
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int e = 8 * i + 2 * j;
+                w[j] = mine ? pack_b16(__uint_as_float(v[e]), __uint_as_float(v[e + 1])) : 0u;
+              }
+              put(at64(0, i), w[0], w[1], w[2], w[3]);
+            }
+            stored([&] { store(&tm_d, 0, col, kSched == Sched::Blocks ? 0 : t.z, false); });
           }
         }
         if (!ok) break;
@@ -879,7 +915,7 @@ int launch_tile_gemm(const char* nm, const GemmMaps& m, const GemmParams& p, int
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cuda_fail("cudaGetDevice");
   if (dev >= kMaxDevices || !attr_set[dev].load(std::memory_order_relaxed)) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, gemm_smem(kSched, kEpi));
     if (e != cudaSuccess) return cuda_fail(nm, e);
     if (dev < kMaxDevices) attr_set[dev].store(true, std::memory_order_relaxed);
   }
@@ -901,7 +937,7 @@ int launch_tile_gemm(const char* nm, const GemmMaps& m, const GemmParams& p, int
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(static_cast<unsigned>((max_tiles < slots ? max_tiles : slots) * (kPair ? 2 : 1)), 1, 1);
   c.blockDim = dim3(kGThreads, 1, 1);
-  c.dynamicSmemBytes = kGSmem;
+  c.dynamicSmemBytes = gemm_smem(kSched, kEpi);
   c.stream = stream;
   c.attrs = attr;
   c.numAttrs = n;
