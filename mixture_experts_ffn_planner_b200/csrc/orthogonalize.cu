@@ -21,15 +21,19 @@
 // decades.  (Earlier it must not be: B's product with the strong directions
 // has to stay in one matrix product.)
 //
-// A side of at most 64 takes another way, in 64 bits throughout: with X = Q G
-// the iteration runs on S x S matrices alone,
+// A side of at most 64 runs in fp32, without tensor cores (whose fp16 noise the
+// steps may amplify to 1e-2 on matrices of a few rows), as one launch: a
+// cluster of up to 8 CTAs a matrix, each with its share of the longer side in
+// shared memory from the first step to the last.  A step sums G G^T over the
+// cluster through distributed shared memory; everything else is local.
+// Where the longer side does not fit (above 5120) the iteration runs on S x S
+// matrices alone, in 64 bits, with X = Q G,
 //   P = a I + b A + c A A,  Q <- P Q,  A <- P A P     from A = G G^T / (|G| + eps)^2, Q = I / (|G| + eps)
 // (|G|_F^2 is the trace of G G^T), in one block a matrix, between one pass over
-// G for G G^T and one for Q G: 3 launches instead of 17, and no fp16, whose
-// noise the steps may amplify to 1e-2 on matrices of a few rows.  It takes 64
-// bits because G G^T squares G's range, and because P, Q and A commute only up
-// to rounding, which the steps amplify as well: in fp32 a 3 x 5 matrix of rank
-// one plus noise came out 6e-4 off, and 0.3 where Q stood for its transpose.
+// G for G G^T and one for Q G.  That takes 64 bits because G G^T squares G's
+// range, and because P, Q and A commute only up to rounding, which the steps
+// amplify as well: in fp32 a 3 x 5 matrix of rank one plus noise came out 6e-4
+// off, and 0.3 where Q stood for its transpose.
 //
 // |G|_F of a larger side is summed in 64 bits.  Every sum has a fixed order.  The launches of a call are
 // chained by programmatic dependent launch.
@@ -310,6 +314,197 @@ __global__ void __launch_bounds__(kNsThreads)
   }
 }
 
+// ------------------------------------- a side of at most 64, the longer one in shared memory
+constexpr int kNsClusterLen = 640;                     // places of the longer side a CTA
+constexpr int kNsClusterMax = 8 * kNsClusterLen;
+constexpr int kNsMatSmem = kNsSmall * static_cast<int>(sizeof(NsRow32));
+
+__device__ __forceinline__ float4 ld_dsmem4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_dsmem4(uint32_t addr, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
+}
+
+// acc[r][s] += sum over k < n of x[k][i0 + r] * x[k][j0 + s]
+__device__ __forceinline__ void ns_outer32(const NsRow32* x, int n, int i0, int j0, float (&acc)[4][4]) {
+#pragma unroll 8
+  for (int k = 0; k < n; ++k) {
+    const float4 u4 = *reinterpret_cast<const float4*>(&x[k][i0]), v4 = *reinterpret_cast<const float4*>(&x[k][j0]);
+    const float u[4] = {u4.x, u4.y, u4.z, u4.w}, v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) acc[r][s] = fmaf(u[r], v[s], acc[r][s]);
+  }
+}
+
+// A cluster a matrix; `per` places of the longer side a CTA, lc >= per a
+// multiple of 64.  Bound by fp32 issue: 64 x 64 takes 5 steps of three products
+// of 64^3 at 128 fmas a clock, 17 us; in 64 bits on one CTA it took 139.
+__global__ void __launch_bounds__(kNsThreads)
+    ns_cluster_kernel(const NsSide n, int per, int lc, int steps, float a, float b, float c, double eps,
+                      __nv_bfloat16* out) {
+  extern __shared__ __align__(16) uint8_t ns_smem[];
+  NsRow32* A = reinterpret_cast<NsRow32*>(ns_smem);
+  NsRow32* P = A + kNsSmall;
+  NsRow32* X = P + kNsSmall;  // [l][i]
+  __shared__ double warps[kNsThreads / 32];
+  __shared__ double norm2;
+  const int tid = threadIdx.x;
+  const uint32_t rank = cluster_ctarank(), ranks = cluster_nctarank();
+  const int64_t z = blockIdx.y;
+  const int base = static_cast<int>(rank) * per;
+  const int nl = max(0, min(per, n.len - base));  // this CTA's places
+  double sum = 0.0;
+  for (int l0 = 0; l0 < lc; l0 += kNsSmall)
+    for (int e = tid; e < kNsSmall * kNsSmall; e += kNsThreads) {
+      const int i = n.i_of(e), l = l0 + n.l_of(e);
+      const float v = i < n.side && l < nl ? ns_load(n.g, n.f32, n.at(z, i, base + l)) : 0.f;
+      X[l][i] = v;
+      sum += static_cast<double>(v) * static_cast<double>(v);
+    }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  if ((tid & 31) == 0) warps[tid >> 5] = sum;
+  __syncthreads();
+  if (tid == 0) {
+    double s = 0.0;
+    for (int w = 0; w < kNsThreads / 32; ++w) s += warps[w];
+    norm2 = s;
+  }
+  __syncthreads();
+  double total = 0.0;
+  if (ranks > 1) {
+    cluster_sync();
+    for (uint32_t q = 0; q < ranks; ++q) {
+      double v;
+      asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(cluster_addr(&norm2, q)) : "memory");
+      total += v;
+    }
+  } else {
+    total = norm2;
+  }
+  const double inv = 1.0 / (sqrt(total) + eps);
+  for (int e = tid; e < nl * kNsSmall; e += kNsThreads) {
+    float* x = &X[e / kNsSmall][e % kNsSmall];
+    *x = static_cast<float>(static_cast<double>(*x) * inv);
+  }
+  __syncthreads();
+  const int ty = tid / 16, tx = tid % 16, i0 = ty * 4, j0 = tx * 4;
+  const bool works = i0 < n.side && j0 < n.side;
+  for (int step = 0; step < steps; ++step) {
+    // A = X X^T, summed over the cluster by slices of rows
+    {
+      NsRow32* dst = ranks > 1 ? P : A;
+      float acc[4][4] = {};
+      if (works) ns_outer32(X, nl, i0, j0, acc);
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        *reinterpret_cast<float4*>(&dst[i0 + r][j0]) = make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
+    }
+    if (ranks > 1) {
+      cluster_sync();
+      const int rows = kNsSmall / static_cast<int>(ranks);
+      for (int e = tid; e < rows * (kNsSmall / 4); e += kNsThreads) {
+        const int i = static_cast<int>(rank) * rows + e / (kNsSmall / 4), j = e % (kNsSmall / 4) * 4;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (uint32_t q = 0; q < ranks; ++q) {
+          const float4 v = ld_dsmem4(cluster_addr(&P[i][j], q));
+          s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+        }
+        for (uint32_t q = 0; q < ranks; ++q) st_dsmem4(cluster_addr(&A[i][j], q), s);
+      }
+      cluster_sync();
+    } else {
+      __syncthreads();
+    }
+    // P = a I + b A + c A A
+    if (works) {
+      float acc[4][4] = {};
+      ns_outer32(A, n.side, i0, j0, acc);
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          P[i0 + r][j0 + s] = fmaf(c, acc[r][s], fmaf(b, A[i0 + r][j0 + s], i0 + r == j0 + s ? a : 0.f));
+    }
+    __syncthreads();
+    // X <- P X, 64 places at a time: 4 places by 4 rows a thread
+    for (int l0 = 0; l0 < nl; l0 += kNsSmall) {
+      float acc[4][4] = {};
+      const bool live = l0 + i0 < nl && j0 < n.side;
+      if (live) {
+#pragma unroll 2
+        for (int k = 0; k < n.side; k += 4) {  // X is zero from the side on
+          float xv[4][4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float4 v = *reinterpret_cast<const float4*>(&X[l0 + i0 + r][k]);
+            xv[r][0] = v.x; xv[r][1] = v.y; xv[r][2] = v.z; xv[r][3] = v.w;
+          }
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const float4 p4 = *reinterpret_cast<const float4*>(&P[k + kk][j0]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              acc[r][0] = fmaf(xv[r][kk], p4.x, acc[r][0]);
+              acc[r][1] = fmaf(xv[r][kk], p4.y, acc[r][1]);
+              acc[r][2] = fmaf(xv[r][kk], p4.z, acc[r][2]);
+              acc[r][3] = fmaf(xv[r][kk], p4.w, acc[r][3]);
+            }
+          }
+        }
+      }
+      __syncthreads();
+      if (live) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          *reinterpret_cast<float4*>(&X[l0 + i0 + r][j0]) = make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
+      }
+    }
+    __syncthreads();
+  }
+  for (int l0 = 0; l0 < nl; l0 += kNsSmall)
+    for (int e = tid; e < kNsSmall * kNsSmall; e += kNsThreads) {
+      const int i = n.i_of(e), l = l0 + n.l_of(e);
+      if (i < n.side && l < nl) out[n.at(z, i, base + l)] = __float2bfloat16_rn(X[l][i]);
+    }
+  if (ranks > 1) cluster_sync();  // no CTA leaves while another may still read its sums
+}
+
+static int run_ns_cluster(const char* nm, const void* g, int f32, int E, int M, int N, int steps, float a, float b,
+                          float c, float eps, void* out, cudaStream_t stream) {
+  const NsSide n{g, f32, M > N ? 1 : 0, std::min(M, N), std::max(M, N)};
+  const int ranks = n.len > 4 * kNsSmall ? 8 : n.len > 2 * kNsSmall ? 4 : n.len > kNsSmall ? 2 : 1;
+  const int per = (n.len + ranks - 1) / ranks;
+  const int lc = (per + kNsSmall - 1) / kNsSmall * kNsSmall;
+  cudaError_t err = cudaFuncSetAttribute(ns_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         2 * kNsMatSmem + kNsClusterLen * static_cast<int>(sizeof(NsRow32)));
+  if (err != cudaSuccess) return cuda_fail(nm, err);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ranks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ranks, E, 1);
+  cfg.blockDim = dim3(kNsThreads, 1, 1);
+  cfg.dynamicSmemBytes = 2 * kNsMatSmem + lc * sizeof(NsRow32);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  err = cudaLaunchKernelEx(&cfg, ns_cluster_kernel, n, per, lc, steps, a, b, c, static_cast<double>(eps),
+                           static_cast<__nv_bfloat16*>(out));
+  return err == cudaSuccess ? MOE_OK : cuda_fail(nm, err);
+}
+
+// ------------------------------------- a side of at most 64, any length: S x S matrices alone
 static int ns_small_chunks(int M, int N) { return std::min((std::max(M, N) + kNsSmall - 1) / kNsSmall, kNsSmallChunks); }
 
 static int run_ns_small(const char* nm, const void* g, int f32, int E, int M, int N, int steps, float a, float b,
@@ -516,6 +711,8 @@ extern "C" int moe_orthogonalize(const void* g, int g_dtype, int E, int M, int N
 
   const int64_t mn = int64_t(M) * N;
   const int f32 = g_dtype == MOE_ROWS_FP32 ? 1 : 0;
+  if (std::min(M, N) <= kNsSmall && std::max(M, N) <= kNsClusterMax)
+    return run_ns_cluster(nm, g, f32, E, M, N, steps, a, b, c, eps, out, n.stream);
   if (std::min(M, N) <= kNsSmall) return run_ns_small(nm, g, f32, E, M, N, steps, a, b, c, eps, out, n.ws, n.stream);
   const bool al = reinterpret_cast<uintptr_t>(g) % 16 == 0;
   double* part = reinterpret_cast<double*>(n.ws + n.L.part);

@@ -76,6 +76,18 @@ def test_larger_matrices():
         check(moe.moe_orthogonalize(g), reference(g))
 
 
+@pytest.mark.parametrize("E,M,N", [(1, 64, 65), (3, 17, 130), (2, 256, 61), (4, 64, 257), (2, 2, 640), (1, 5120, 64),
+                                   (1, 64, 5121), (2, 63, 9000), (150, 40, 500)])
+def test_short_sides(E, M, N):
+    """Every way of a side of at most 64: one CTA a matrix, clusters of 2, 4 and 8, and a side too long for them."""
+    import mixture_experts_ffn_planner_b200 as moe
+
+    for kind in ("lowrank", "decades"):
+        g = matrices(E, M, N, kind, "float32")
+        check(moe.moe_orthogonalize(g), reference(g))
+    moe.moe_device_status()
+
+
 @pytest.mark.parametrize("E,M,N", [(80, 100, 300), (75, 300, 72), (20, 520, 700), (19, 777, 513)])
 def test_many_matrices(E, M, N):
     """Enough tiles for every pair of SMs, with tails on both sides."""
