@@ -26,7 +26,12 @@
 
 namespace moe {
 
+// Threads a block.  With dot products a thread holds a row's vectors of x, y
+// and the products (108 registers): blocks of 128 then fill an SM better (8192
+// tokens of 8 KB, top 8: 199 us, 217 at 256); without, 256 are ahead where
+// there are few tokens (64 tokens of 16 KB: 12 and 16 us).
 constexpr int kPermThreads = 256;
+constexpr int kPermGradThreads = 128;
 constexpr int kPermJ = 8;  // routes handled at once (registers); more routes take another turn
 
 template <typename T>
@@ -68,10 +73,21 @@ __device__ __forceinline__ Vec<T, VB> load_vec(const T* row, int v) {
   r.raw = __ldg(reinterpret_cast<const typename Raw<VB>::type*>(row) + v);
   return r;
 }
+// The same for what nothing reads again (8192 tokens of 8 KB gathered: 104.5 us, 106.5 without the hint).
+template <typename T, int VB>
+__device__ __forceinline__ Vec<T, VB> load_vec_once(const T* row, int v) {
+  Vec<T, VB> r;
+  r.raw = __ldcs(reinterpret_cast<const typename Raw<VB>::type*>(row) + v);
+  return r;
+}
 template <typename T, int VB>
 __device__ __forceinline__ void store_vec(T* row, int v, const Vec<T, VB>& x) {
   reinterpret_cast<typename Raw<VB>::type*>(row)[v] = x.raw;
 }
+
+// Vectors of a row that a thread handles at once, a block's width apart: the
+// narrow ones of odd row lengths need several to have as many bytes in flight.
+constexpr int row_unroll(int vb) { return vb == 16 ? 1 : vb == 8 ? 2 : 4; }
 
 struct ScatterParams {
   const void* token;           // (T, K): x, or grad_out
@@ -83,13 +99,15 @@ struct ScatterParams {
   void* row_out;               // (capacity, K)
   float* grad_w;               // (T, top_k), or null
   int64_t capacity;
-  int T, top_k, K, tpt, pad_blocks, pad_step;
+  int T, top_k, K, tpt, chunks, span, pad_blocks, pad_step;
 };
 
 // Blocks [0, pad_blocks) write zeros into the padding rows below the padded
-// total; the others own kPermThreads / tpt tokens each, tpt threads a token.
+// total; the others own threads / tpt tokens each, tpt threads a token, or one
+// of `chunks` parts (span vectors) of a token's row.
 template <typename T, int VB, bool kGrad>
-__global__ void __launch_bounds__(kPermThreads) row_scatter_kernel(const ScatterParams p) {
+__global__ void __launch_bounds__(kGrad ? kPermGradThreads : kPermThreads) row_scatter_kernel(const ScatterParams p) {
+  constexpr int kThreads = kGrad ? kPermGradThreads : kPermThreads, kU = row_unroll(VB);
   using V = Vec<T, VB>;
   const int nv = p.K / V::n;
   const int64_t R = static_cast<int64_t>(p.T) * p.top_k;
@@ -97,8 +115,8 @@ __global__ void __launch_bounds__(kPermThreads) row_scatter_kernel(const Scatter
     // one warp looks at pad_step (at most 32) places at a time and clears the rows of those that hold no route
     const int lane = threadIdx.x & 31;
     const int64_t total = min(static_cast<int64_t>(max(__ldg(p.ntpp), 0)), p.capacity);
-    const int64_t warps = static_cast<int64_t>(p.pad_blocks) * (kPermThreads / 32);
-    for (int64_t p0 = (static_cast<int64_t>(blockIdx.x) * (kPermThreads / 32) + (threadIdx.x >> 5)) * p.pad_step;
+    const int64_t warps = static_cast<int64_t>(p.pad_blocks) * (kThreads / 32);
+    for (int64_t p0 = (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * p.pad_step;
          p0 < total; p0 += warps * p.pad_step) {
       bool pad = false;
       if (lane < p.pad_step && p0 + lane < total) {
@@ -115,10 +133,12 @@ __global__ void __launch_bounds__(kPermThreads) row_scatter_kernel(const Scatter
     }
     return;
   }
-  __shared__ float part[kPermThreads / 32][kPermJ];
-  const int per = kPermThreads / p.tpt;
+  __shared__ float part[kThreads / 32][kPermJ];
+  const int per = kThreads / p.tpt;
   const int sub = threadIdx.x / p.tpt, tid = threadIdx.x - sub * p.tpt;
-  const int64_t t = (static_cast<int64_t>(blockIdx.x) - p.pad_blocks) * per + sub;
+  const uint32_t place = blockIdx.x - static_cast<uint32_t>(p.pad_blocks), chunks = static_cast<uint32_t>(p.chunks);
+  const int64_t t = static_cast<int64_t>(kGrad ? place : place / chunks) * per + sub;  // a dot product takes the whole row
+  const int v_lo = kGrad ? 0 : static_cast<int>(place % chunks) * p.span, v_hi = kGrad ? nv : min(nv, v_lo + p.span);
   const bool live = t < p.T;
   const T* src = static_cast<const T*>(p.token) + t * p.K;
   for (int j0 = 0; j0 < p.top_k; j0 += kPermJ) {
@@ -136,28 +156,42 @@ __global__ void __launch_bounds__(kPermThreads) row_scatter_kernel(const Scatter
       at[j] = s >= 0 && s < p.capacity ? static_cast<int64_t>(s) * p.K : -1;
     }
     if (live) {
-      for (int v = tid; v < nv; v += p.tpt) {
-        const V x = load_vec<T, VB>(src, v);
+      for (int v0 = v_lo + tid; v0 < v_hi; v0 += kU * p.tpt) {
+        V x[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+          if (u == 0 || v0 + u * p.tpt < v_hi) x[u] = load_vec<T, VB>(src, v0 + u * p.tpt);
         if (kGrad) {
-          V y[kPermJ];
+          V y[kU][kPermJ];
 #pragma unroll
-          for (int j = 0; j < kPermJ; ++j)
-            if (at[j] >= 0) y[j] = load_vec<T, VB>(static_cast<const T*>(p.rows) + at[j], v);
+          for (int u = 0; u < kU; ++u)
 #pragma unroll
-          for (int j = 0; j < kPermJ; ++j) {
-            if (at[j] < 0) continue;
-            V g;
+            for (int j = 0; j < kPermJ; ++j)
+              if (at[j] >= 0 && (u == 0 || v0 + u * p.tpt < v_hi))
+                y[u][j] = load_vec<T, VB>(static_cast<const T*>(p.rows) + at[j], v0 + u * p.tpt);
 #pragma unroll
-            for (int i = 0; i < V::n; ++i) {
-              dot[j] = fmaf(x.get(i), y[j].get(i), dot[j]);
-              g.set(i, w[j] * x.get(i));
+          for (int u = 0; u < kU; ++u) {
+            if (u > 0 && v0 + u * p.tpt >= v_hi) break;
+#pragma unroll
+            for (int j = 0; j < kPermJ; ++j) {
+              if (at[j] < 0) continue;
+              V g;
+#pragma unroll
+              for (int i = 0; i < V::n; ++i) {
+                dot[j] = fmaf(x[u].get(i), y[u][j].get(i), dot[j]);
+                g.set(i, w[j] * x[u].get(i));
+              }
+              store_vec<T, VB>(static_cast<T*>(p.row_out) + at[j], v0 + u * p.tpt, g);
             }
-            store_vec<T, VB>(static_cast<T*>(p.row_out) + at[j], v, g);
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < kPermJ; ++j)
-            if (at[j] >= 0) store_vec<T, VB>(static_cast<T*>(p.row_out) + at[j], v, x);
+          for (int u = 0; u < kU; ++u) {
+            if (u > 0 && v0 + u * p.tpt >= v_hi) break;
+#pragma unroll
+            for (int j = 0; j < kPermJ; ++j)
+              if (at[j] >= 0) store_vec<T, VB>(static_cast<T*>(p.row_out) + at[j], v0 + u * p.tpt, x[u]);
+          }
         }
       }
     }
@@ -189,17 +223,19 @@ struct GatherParams {
   const float* weights;  // (T, top_k), or null
   void* out;             // (T, K)
   int64_t n_rows;
-  int T, top_k, K, tpt;
+  int T, top_k, K, tpt, span;
 };
 
 template <typename T, int VB>
-__global__ void __launch_bounds__(kPermThreads) row_gather_kernel(const GatherParams p) {
+// Three blocks an SM: at two (98 registers) 8192 tokens of 8 KB took 123 us instead of 106.
+__global__ void __launch_bounds__(kPermThreads, 3) row_gather_kernel(const GatherParams p) {
   using V = Vec<T, VB>;
   const int nv = p.K / V::n;
   const int per = kPermThreads / p.tpt;
   const int sub = threadIdx.x / p.tpt, tid = threadIdx.x - sub * p.tpt;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * per + sub;
   if (t >= p.T) return;
+  const int v_lo = static_cast<int>(blockIdx.y) * p.span, v_hi = min(nv, v_lo + p.span);
   const T* rows = static_cast<const T*>(p.rows);
   T* out = static_cast<T*>(p.out) + t * p.K;
   int64_t at[kPermJ];
@@ -217,27 +253,40 @@ __global__ void __launch_bounds__(kPermThreads) row_gather_kernel(const GatherPa
     }
   };
   slots_of(0);
-  for (int v = tid; v < nv; v += p.tpt) {
-    float acc[V::n];
+  constexpr int kU = row_unroll(VB);
+  for (int v0 = v_lo + tid; v0 < v_hi; v0 += kU * p.tpt) {
+    float acc[kU][V::n];
 #pragma unroll
-    for (int i = 0; i < V::n; ++i) acc[i] = 0.f;
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int i = 0; i < V::n; ++i) acc[u][i] = 0.f;
     for (int j0 = 0; j0 < p.top_k; j0 += kPermJ) {
       if (p.top_k > kPermJ) slots_of(j0);
-      V y[kPermJ];
+      V y[kU][kPermJ];
 #pragma unroll
-      for (int j = 0; j < kPermJ; ++j)
-        if (at[j] >= 0) y[j] = load_vec<T, VB>(rows + at[j], v);
+      for (int u = 0; u < kU; ++u)
 #pragma unroll
-      for (int j = 0; j < kPermJ; ++j) {
-        if (at[j] < 0) continue;
+        for (int j = 0; j < kPermJ; ++j)
+          if (at[j] >= 0 && (u == 0 || v0 + u * p.tpt < v_hi)) y[u][j] = load_vec_once<T, VB>(rows + at[j], v0 + u * p.tpt);
 #pragma unroll
-        for (int i = 0; i < V::n; ++i) acc[i] = fmaf(w[j], y[j].get(i), acc[i]);
+      for (int u = 0; u < kU; ++u) {
+        if (u > 0 && v0 + u * p.tpt >= v_hi) break;
+#pragma unroll
+        for (int j = 0; j < kPermJ; ++j) {
+          if (at[j] < 0) continue;
+#pragma unroll
+          for (int i = 0; i < V::n; ++i) acc[u][i] = fmaf(w[j], y[u][j].get(i), acc[u][i]);
+        }
       }
     }
-    V o;
 #pragma unroll
-    for (int i = 0; i < V::n; ++i) o.set(i, acc[i]);
-    store_vec<T, VB>(out, v, o);
+    for (int u = 0; u < kU; ++u) {
+      if (u > 0 && v0 + u * p.tpt >= v_hi) break;
+      V o;
+#pragma unroll
+      for (int i = 0; i < V::n; ++i) o.set(i, acc[u][i]);
+      store_vec<T, VB>(out, v0 + u * p.tpt, o);
+    }
   }
 }
 
@@ -263,10 +312,22 @@ static int vector_bytes(int64_t row_bytes, int esize, std::initializer_list<cons
 
 // Threads per token: a power of two between a warp and the block, enough for
 // one vector each; a short row then shares its block with other tokens.
-static int threads_per_token(int64_t nv) {
+static int threads_per_token(int64_t nv, int threads) {
   int tpt = 32;
-  while (tpt < kPermThreads && tpt < nv) tpt <<= 1;
+  while (tpt < threads && tpt < nv) tpt <<= 1;
   return tpt;
+}
+
+// Parts that a row is split into, of `span` vectors each: while blocks are
+// fewer than 4 an SM, so that a thread has fewer vectors to wait for in turn
+// (64 tokens of 16 KB, top 8, gathered: 12 -> 8 us).
+static int row_chunks(int64_t blocks, int64_t nv, int tpt, int* span) {
+  int64_t n = 1;
+  if (tpt == kPermThreads)
+    while (blocks * n < static_cast<int64_t>(std::max(1, sm_count())) * 4 && n * tpt < nv) n <<= 1;
+  const int64_t s = ((nv + n - 1) / n + tpt - 1) / tpt * tpt;
+  *span = static_cast<int>(s);
+  return static_cast<int>((nv + s - 1) / s);
 }
 
 // Calls f(type tag, integral constant of the access width).
@@ -309,23 +370,30 @@ static int run_scatter(const char* nm, ScatterParams p, int dtype, bool grad, cu
       misaligned({p.sorted_ids, p.ntpp, p.slots, p.weights, p.grad_w}, 4))
     return fail(MOE_ERR_ALIGNMENT, "%s: pointers must be aligned to their element", nm);
   const int vb = vector_bytes(static_cast<int64_t>(p.K) * esize, esize, {p.token, p.rows, p.row_out});
-  p.tpt = threads_per_token(static_cast<int64_t>(p.K) * esize / vb);
-  const int per = kPermThreads / p.tpt;
-  const int64_t token_blocks = (static_cast<int64_t>(p.T) + per - 1) / per;
+  const int threads = grad ? kPermGradThreads : kPermThreads;
+  const int64_t nv = static_cast<int64_t>(p.K) * esize / vb;
+  p.tpt = threads_per_token(nv, threads);
+  const int per = threads / p.tpt;
+  int64_t token_blocks = (static_cast<int64_t>(p.T) + per - 1) / per;
+  p.chunks = 1;
+  if (!grad) {
+    p.chunks = row_chunks(token_blocks, nv, p.tpt, &p.span);
+    token_blocks *= p.chunks;
+  }
   // The padding goes over all SMs, one place a warp while they last: with 32
   // places a warp always, a call of 8 tokens (960 padding rows of 8 KB) took
   // 30 us on 8 blocks.
-  constexpr int kPadWarps = kPermThreads / 32;
-  const int64_t pad_warps = static_cast<int64_t>(std::max(1, sm_count())) * 4 * kPadWarps;
+  const int block_warps = threads / 32;
+  const int64_t pad_warps = static_cast<int64_t>(std::max(1, sm_count())) * 4 * block_warps;
   p.pad_step = static_cast<int>(std::min<int64_t>(std::max<int64_t>((p.capacity + pad_warps - 1) / pad_warps, 1), 32));
   const int64_t pad_warps_used = std::min<int64_t>((p.capacity + p.pad_step - 1) / p.pad_step, pad_warps);
-  p.pad_blocks = static_cast<int>((pad_warps_used + kPadWarps - 1) / kPadWarps);
+  p.pad_blocks = static_cast<int>((pad_warps_used + block_warps - 1) / block_warps);
   const int64_t blocks = token_blocks + p.pad_blocks;
   if (blocks == 0) return MOE_OK;
   const cudaError_t err = by_access(dtype, vb, [&](auto tag, auto width) {
     using T = decltype(tag);
     if (grad)
-      row_scatter_kernel<T, decltype(width)::value, true><<<static_cast<unsigned>(blocks), kPermThreads, 0, s>>>(p);
+      row_scatter_kernel<T, decltype(width)::value, true><<<static_cast<unsigned>(blocks), kPermGradThreads, 0, s>>>(p);
     else
       row_scatter_kernel<T, decltype(width)::value, false><<<static_cast<unsigned>(blocks), kPermThreads, 0, s>>>(p);
     return cudaGetLastError();
@@ -338,11 +406,13 @@ static int run_gather(const char* nm, GatherParams p, int dtype, cudaStream_t s)
   if (misaligned({p.rows, p.out}, esize) || misaligned({p.slots, p.weights}, 4))
     return fail(MOE_ERR_ALIGNMENT, "%s: pointers must be aligned to their element", nm);
   const int vb = vector_bytes(static_cast<int64_t>(p.K) * esize, esize, {p.rows, p.out});
-  p.tpt = threads_per_token(static_cast<int64_t>(p.K) * esize / vb);
+  const int64_t nv = static_cast<int64_t>(p.K) * esize / vb;
+  p.tpt = threads_per_token(nv, kPermThreads);
   const int per = kPermThreads / p.tpt;
   const int64_t blocks = (static_cast<int64_t>(p.T) + per - 1) / per;
+  const dim3 grid(static_cast<unsigned>(blocks), row_chunks(blocks, nv, p.tpt, &p.span));
   const cudaError_t err = by_access(dtype, vb, [&](auto tag, auto width) {
-    row_gather_kernel<decltype(tag), decltype(width)::value><<<static_cast<unsigned>(blocks), kPermThreads, 0, s>>>(p);
+    row_gather_kernel<decltype(tag), decltype(width)::value><<<grid, kPermThreads, 0, s>>>(p);
     return cudaGetLastError();
   });
   return err == cudaSuccess ? MOE_OK : cuda_fail(nm, err);
