@@ -555,8 +555,9 @@ static NsLayout ns_layout(int E, int M, int N) {
   }
   auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b * b; };
   L.side = std::min(M, N);
-  L.ldx = static_cast<int>(up(N, 8));
-  L.lds = static_cast<int>(up(L.side, 8));
+  // rows begin on 128 bytes: an operand row of 128 bytes is then one line of L2
+  L.ldx = static_cast<int>(up(N, 64));
+  L.lds = static_cast<int>(up(L.side, 64));
   L.chunks = static_cast<int>(std::min<int64_t>((static_cast<int64_t>(M) * N + 8 * kNsThreads - 1) / (8 * kNsThreads), kNsChunks));
   const int64_t x = up(static_cast<int64_t>(E) * M * L.ldx * 2, 256), s = up(static_cast<int64_t>(E) * L.side * L.lds * 2, 256);
   int64_t off = 0;

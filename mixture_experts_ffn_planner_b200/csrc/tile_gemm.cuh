@@ -591,7 +591,12 @@ __global__ void __launch_bounds__(kGThreads, 1)
       const int col0 = t.n0 + (kEpi == Epi::GateUp ? hf * (kHalfCols / 2) : hf * kHalfCols);
       bool mine = r < t.limit;  // this thread's row carries a value (a padding row: zeros)
       if (kSched == Sched::Blocks && mine) mine = __ldg(p.sorted_ids + static_cast<int64_t>(t.m0) + r) >= 0;
-      if (kSide && rows_here && col0 < p.n_total) side_load(piece & 1, col0);
+      // the first piece, while the MMAs run, or both of a single CTA (of a pair a second one only adds to the load:
+      // 228 us an update of 16 x 2048 x 2048, 212 without)
+      if (kSide && rows_here) {
+        if (col0 < p.n_total) side_load(piece & 1, col0);
+        if (!kPair && col0 + 32 < p.n_total) side_load((piece & 1) ^ 1, col0 + 32);
+      }
       const int buf = acc_it & 1;
       if (t.nk > 0) {
         ok = wait(&acc_full[buf], (acc_it >> 1) & 1);
@@ -655,7 +660,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
             const int col = col0 + 32 * c;
             if (col >= p.n_total) break;
             const int b = piece & 1;
-            if (c + 1 < kHalfCols / 32 && col + 32 < p.n_total) side_load(b ^ 1, col + 32);
+            if ((kPair || c > 0) && c + 1 < kHalfCols / 32 && col + 32 < p.n_total) side_load(b ^ 1, col + 32);
             uint32_t v[32];
             acc32(hf * kHalfCols + 32 * c, v);
             ok = mbar_wait(&side[b], (side_ph >> b) & 1u, abort_flag, p.status, p.wait_ns);
