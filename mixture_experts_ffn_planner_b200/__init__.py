@@ -571,7 +571,7 @@ def _call(fn, dev, stream, *args):
     of 8 tokens with one, and with every check of _tensor made on its own)."""
     import torch
 
-    if stream is None and dev.type == "cuda" and dev.index == torch._C._cuda_getDevice():
+    if stream is None and dev.index == torch._C._cuda_getDevice() and dev.type == "cuda":
         rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     else:
         with _on_device(dev, stream) as s:
@@ -597,8 +597,8 @@ def _new(shape, dtype, dev, stream):
 
 def _tensor(t, name, dtype, dev, shape):
     """One argument of a training call: type, layout, device and shape (the kernels trust all four)."""
-    if t is not None and t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous() and t.is_cuda:
-        return
+    if t is not None and t.dtype is dtype and t.get_device() == dev.index and t.shape == shape and t.is_contiguous():
+        return  # (the index of a CPU tensor is -1, that of its device None)
     if t is None:
         raise ValueError(f"{name} is required")
     if t.dtype != dtype:

@@ -15,13 +15,28 @@
 
 namespace moe {
 
-// Pairs of CTAs take tiles of 256 x 256, single ones 128 x 128, with twice the
-// bytes from L2 a flop but four times as many tiles.  Single against pair, us,
-// at K = N = 2048 on 64 experts: up 218 and 172 at 256 rows an expert, 676 and
-// 469 at 1024, 27 and 31 at 16; at K = 4096, N = 512 on 8 experts, where pairs
-// have 16 tiles, 35 and 39 at 256 rows.
-constexpr int64_t kPairRows = 192;   // rows an expert from which a 256-row tile is filled well enough
-constexpr int64_t kPairTiles = 37;   // tiles that keep half of the pairs busy
+// Pairs of CTAs take tiles of 256 x 256, single ones 128 x 128 with twice the
+// bytes from L2 a flop, but four times as many tiles that end four times as
+// soon.  So pairs are for tiles that are many, filled well and long.  Single
+// and pair, us, on 40 experts: up at K = N = 2048, 84 and 86 with 64 rows an
+// expert, 102 and 96 with 192, 512 and 389 with 1536; down at K = 4096, N = 512
+// (a contraction of 256), 70 and 90 with 384 rows, 213 and 218 with 1536; up at
+// K = 4096, N = 512 on 8 experts, 33 and 37 with 384 rows (32 tiles of pairs).
+// Where a row's pitch is no multiple of 128 bytes, every 128 of an operand lie
+// in two lines of L2 and the bytes count for more: down at K = 1992, N = 1360,
+// 57 and 51 with 128 rows, 88 and 62 with 256.
+constexpr int64_t kPairTiles = 48;
+static bool pairs_for_rows(int64_t tiles, int64_t rows, int64_t contraction, bool lines) {
+  if (tiles < kPairTiles) return false;
+  if (!lines) return rows >= 128 && rows * contraction >= 80 * 1024;
+  return rows >= 192 && rows * contraction >= (contraction >= 512 ? 128 : 384) * 1024;
+}
+// Weight gradients, whose contraction is the rows: up_backward at K = 4096,
+// N = 1024 on 40 experts, 224 and 230 us with 192 rows, 302 and 286 with 384;
+// at K = 1000, N = 992, 93 and 91, 138 and 122.
+static bool pairs_for_weights(int64_t tiles, int64_t rows, bool lines) {
+  return tiles >= kPairTiles && rows >= (lines ? 256 : 192);
+}
 
 struct ExpertCall {
   const char* nm;
@@ -139,12 +154,13 @@ static int blocks_tiled(const ExpertCall& c, const void* in, int64_t width_in, c
 
 // cols: columns of the product.
 template <Form kForm, Epi kEpi, typename... Args>
-static int run_blocks(const ExpertCall& c, int64_t cols, Args... args) {
+static int run_blocks(const ExpertCall& c, int64_t cols, const void* in, int64_t width_in, Args... args) {
   if (c.capacity / c.bm == 0) return MOE_OK;
   const int64_t rows = mean_rows(c);
-  return rows >= kPairRows && c.E * ceil_div(rows, 256) * ceil_div(cols, 256) >= kPairTiles
-             ? blocks_tiled<kForm, kEpi, true>(c, args...)
-             : blocks_tiled<kForm, kEpi, false>(c, args...);
+  const bool lines = width_in % 64 == 0 && (kForm != Form::NN || cols % 64 == 0);
+  return pairs_for_rows(c.E * ceil_div(rows, 256) * ceil_div(cols, 256), rows, width_in, lines)
+             ? blocks_tiled<kForm, kEpi, true>(c, in, width_in, args...)
+             : blocks_tiled<kForm, kEpi, false>(c, in, width_in, args...);
 }
 
 // grad[e] (m x n) = sum over e's rows of a^T b, a (capacity, m), b (capacity, n).
@@ -175,7 +191,7 @@ static int weights_tiled(const ExpertCall& c, const void* a, int64_t m, const vo
 
 static int run_weights(const ExpertCall& c, const void* a, int64_t m, const void* b, int64_t n, void* grad, int f32,
                        int accumulate) {
-  return c.E * ceil_div(m, 256) * ceil_div(n, 256) >= kPairTiles
+  return pairs_for_weights(c.E * ceil_div(m, 256) * ceil_div(n, 256), mean_rows(c), m % 64 == 0 && n % 64 == 0)
              ? weights_tiled<true>(c, a, m, b, n, grad, f32, accumulate)
              : weights_tiled<false>(c, a, m, b, n, grad, f32, accumulate);
 }
