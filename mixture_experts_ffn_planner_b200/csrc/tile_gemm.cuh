@@ -147,7 +147,7 @@ __device__ __forceinline__ void find_segments(const GemmParams& p, int blocks, i
 }
 
 // The tiles of one role, in the order that every role walks them: tile numbers
-// `first`, first + stride, ... (warp-collective).
+// `from`, from + stride, ... (warp-collective).
 template <Sched kSched, Epi kEpi, bool kPair>
 struct Walk {
   static constexpr int kCols = kEpi == Epi::GateUp ? tile_n(kPair) / 2 : tile_n(kPair);
@@ -164,10 +164,8 @@ struct Walk {
   int z_next = -1;
   int last_ids[4];
 
-  __device__ __forceinline__ Walk(const GemmParams& p_, int rank_, int blocks_, const int* first_)
-      : p(p_), lane(static_cast<int>(lane_id())), rank(rank_), stride(kPair ? gridDim.x / 2 : gridDim.x), blocks(blocks_),
-        first(first_) {
-    u = kPair ? blockIdx.x / 2 : blockIdx.x;
+  __device__ __forceinline__ Walk(const GemmParams& p_, int rank_, int from, int stride_, int blocks_, const int* first_)
+      : p(p_), lane(static_cast<int>(lane_id())), rank(rank_), stride(stride_), blocks(blocks_), u(from), first(first_) {
     per_z = kSym ? p.m_tiles * (p.m_tiles + 1) / 2 : p.m_tiles * p.n_tiles;
     units = p.batches * per_z;
     if (kSched == Sched::Blocks) look(0);
@@ -266,34 +264,112 @@ struct Walk {
 // routed rows: from row `rem` of 64 on; 64 or more: nothing.
 __device__ __forceinline__ bool ragged(const Tile& t, int kc) { return t.rows - kc * kGK < kGK; }
 
-template <Form kForm, Sched kSched, Epi kEpi, bool kPair, bool kBf16>
-__global__ void __launch_bounds__(kGThreads, 1)
-    tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                     const __grid_constant__ CUtensorMap tm_d, const __grid_constant__ CUtensorMap tm_d2,
-                     const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_c2,
-                     const __grid_constant__ GemmParams p) {
+// A thread's view of its CTA: the shared memory's parts, and where its warp's
+// role stands in the rings, which go on from one product to the next.
+struct TileCta {
+  uint8_t* smem;
+  uint64_t *full, *empty;
+  uint64_t* part;       // ragged chunks: landed, not yet cleared
+  uint64_t *acc_full, *acc_empty;
+  uint64_t* side_full;  // [kGEpiWarps][2]
+  uint32_t* tmem_base_sm;
+  volatile int* abort_flag;
+  int warp, lane;
+  uint32_t rank, tbase;
+  int s, acc_it, piece, count;
+  uint32_t ph, side_ph, seen;
+};
+
+// Shared memory's layout, barriers, TMEM; the CTA's other set-up may follow before tile_cta_ready.
+template <int kStages, int kBuf, bool kPair>
+__device__ __forceinline__ void tile_cta_setup(TileCta* c, uint8_t* smem_raw) {
+  c->smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  c->full = reinterpret_cast<uint64_t*>(c->smem + kStages * kGStage + kGEpiWarps * 2 * kBuf);
+  c->empty = c->full + kStages;
+  c->part = c->empty + kStages;
+  c->acc_full = c->part + kStages;
+  c->acc_empty = c->acc_full + 2;
+  c->side_full = c->acc_empty + 2;
+  c->tmem_base_sm = reinterpret_cast<uint32_t*>(c->side_full + 2 * kGEpiWarps);
+  c->abort_flag = reinterpret_cast<volatile int*>(c->tmem_base_sm + 1);
+  // by shuffle, so that the compiler knows them to be the same in all lanes, and the roles' operands to be uniform
+  c->warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+  c->lane = threadIdx.x & 31;
+  c->rank = kPair ? cluster_ctarank() : 0u;
+  c->s = c->acc_it = c->piece = c->count = 0;
+  c->ph = c->side_ph = c->seen = 0;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      // pair: the even CTA's twice, for the copies of both, or warp 10 of each
+      mbar_init(&c->full[s], kPair ? 2 : 1);
+      mbar_init(&c->empty[s], 1);
+      mbar_init(&c->part[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&c->acc_full[a], 1);
+      mbar_init(&c->acc_empty[a], kPair ? 2 * kGEpiWarps : kGEpiWarps);
+    }
+    for (int i = 0; i < 2 * kGEpiWarps; ++i) mbar_init(&c->side_full[i], 1);
+    *c->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (c->warp == 1) {
+    if (kPair) {
+      tmem_alloc_pair(c->tmem_base_sm, 2 * tile_n(kPair));
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(c->tmem_base_sm, 2 * tile_n(kPair));
+      tmem_relinquish();
+    }
+  }
+}
+template <bool kPair>
+__device__ __forceinline__ void tile_cta_ready(TileCta* c) {
+  tc_fence_before();
+  __syncthreads();
+  if (kPair) cluster_sync();  // the other CTA's barriers are ready
+  tc_fence_after();
+  c->tbase = __shfl_sync(0xffffffffu, *c->tmem_base_sm, 0);
+}
+template <bool kPair>
+__device__ __forceinline__ void tile_cta_leave(const TileCta& c) {
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (*c.abort_flag) {
+    // copies and MMAs issued before a wait gave up may still be landing; they
+    // finish within microseconds
+    const unsigned long long t0 = globaltimer();
+    while (globaltimer() - t0 < 100000ull) __nanosleep(1000);
+  }
+  __syncwarp();
+  if (kPair) cluster_sync();  // neither CTA leaves while the other may still read or signal it
+  if (c.warp == 1) {
+    tc_fence_after();
+    if (kPair)
+      tmem_dealloc_pair(c.tbase, 2 * tile_n(kPair));
+    else
+      tmem_dealloc(c.tbase, 2 * tile_n(kPair));
+  }
+}
+
+// One product: every warp in its role over the tiles of `walk`.
+template <Form kForm, Sched kSched, Epi kEpi, bool kPair, bool kBf16, int kStages, int kBuf>
+__device__ __forceinline__ void tile_product(TileCta& c, Walk<kSched, kEpi, kPair>& walk, const CUtensorMap* tm_a,
+                                             const CUtensorMap* tm_b, const CUtensorMap* tm_d, const CUtensorMap* tm_d2,
+                                             const CUtensorMap* tm_c, const CUtensorMap* tm_c2, const GemmParams& p) {
   constexpr int kN = tile_n(kPair);
-  constexpr uint32_t kTmemCols = 2 * kN;
   constexpr bool kAMn = kForm == Form::TN, kBMn = kForm != Form::NT;
-  constexpr int kStages = gemm_stages(kSched, kEpi), kBuf = gemm_buf(kEpi);
-  constexpr int kStaging = kStages * kGStage, kCtrl = gemm_ctrl(kSched, kEpi);
+  constexpr int kStaging = kStages * kGStage;
   // side tiles of 32 columns, one or two at once
   constexpr bool kSide = epi_side(kEpi);
   constexpr int kSideTiles = kEpi == Epi::Poly ? 1 : 2;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kCtrl);
-  uint64_t* empty = full + kStages;
-  uint64_t* part = empty + kStages;      // ragged chunks: landed, not yet cleared
-  uint64_t* acc_full = part + kStages;
-  uint64_t* acc_empty = acc_full + 2;
-  uint64_t* side_full = acc_empty + 2;    // [kGEpiWarps][2]
-  uint32_t* tmem_base_sm = reinterpret_cast<uint32_t*>(side_full + 2 * kGEpiWarps);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_sm + 1);
-  int* first = reinterpret_cast<int*>(smem + kCtrl + kGCtrlBytes);
-  // by shuffle, so that the compiler knows them to be the same in all lanes, and the roles' operands to be uniform
-  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const uint32_t rank = kPair ? cluster_ctarank() : 0u;
+  uint8_t* const smem = c.smem;
+  uint64_t *const full = c.full, *const empty = c.empty, *const part = c.part;
+  uint64_t *const acc_full = c.acc_full, *const acc_empty = c.acc_empty, *const side_full = c.side_full;
+  volatile int* const abort_flag = c.abort_flag;
+  const int warp = c.warp, lane = c.lane;
+  const uint32_t rank = c.rank, tbase = c.tbase;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return mbar_wait(bar, parity, abort_flag, p.status, p.wait_ns);
   };
@@ -302,56 +378,13 @@ __global__ void __launch_bounds__(kGThreads, 1)
   auto wait_cluster = [&](uint64_t* bar, uint32_t parity) {
     return mbar_wait<kPair>(bar, parity, abort_flag, p.status, p.wait_ns);
   };
-
-  pdl_launch_dependents();
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      // pair: the even CTA's twice, for the copies of both, or warp 10 of each
-      mbar_init(&full[s], kPair ? 2 : 1);
-      mbar_init(&empty[s], 1);
-      mbar_init(&part[s], 1);
-    }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(&acc_full[a], 1);
-      mbar_init(&acc_empty[a], kPair ? 2 * kGEpiWarps : kGEpiWarps);
-    }
-    for (int i = 0; i < 2 * kGEpiWarps; ++i) mbar_init(&side_full[i], 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-    prefetch_tmap(&tm_a);
-    prefetch_tmap(&tm_b);
-    prefetch_tmap(&tm_d);
-    if (kSide) prefetch_tmap(&tm_c);
-  }
-  if (warp == 1) {
-    if (kPair) {
-      tmem_alloc_pair(tmem_base_sm, kTmemCols);
-      tmem_relinquish_pair();
-    } else {
-      tmem_alloc(tmem_base_sm, kTmemCols);
-      tmem_relinquish();
-    }
-  }
-  int blocks = 0;
-  if (kSched != Sched::Batch) {  // the plan; these launches are not chained
-    const int n = __ldg(p.ntpp) / p.bm;
-    blocks = n < 0 ? 0 : min(n, p.max_blocks);
-    if (kSched == Sched::Experts) find_segments(p, blocks, first);
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (kPair) cluster_sync();  // the other CTA's barriers are ready
-  tc_fence_after();
-  const uint32_t tbase = __shfl_sync(0xffffffffu, *tmem_base_sm, 0);
-  if (kSched == Sched::Batch) pdl_wait();  // what a chained launch before this one wrote is read below
-  Walk<kSched, kEpi, kPair> walk(p, static_cast<int>(rank), blocks, first);
   Tile t;
 
   if (warp == 0) {
     // ------------------------------------------------ TMA producer
     const uint64_t pol = policy_evict_normal();
-    int s = 0;
-    uint32_t ph = 0;
+    int s = c.s;
+    uint32_t ph = c.ph;
     bool ok = true;
     while (ok && walk.next(&t)) {
       const int za = kSched == Sched::Batch ? t.z : 0;
@@ -383,34 +416,36 @@ __global__ void __launch_bounds__(kGThreads, 1)
               tma_load_3d(dst, map, held ? &part[s] : &full[s], c0, c1, c2, pol);
           };
           if (kAMn) {
-            load(a, &tm_a, t.m0, k0, za);
-            load(a + kGHalf / 2, &tm_a, t.m0 + 64, k0, za);
+            load(a, tm_a, t.m0, k0, za);
+            load(a + kGHalf / 2, tm_a, t.m0 + 64, k0, za);
           } else {
-            for (int i = 0; i < boxes; ++i) load(a + i * p.a_rows * kGRow, &tm_a, k0, t.m0 + i * p.a_rows, za);
+            for (int i = 0; i < boxes; ++i) load(a + i * p.a_rows * kGRow, tm_a, k0, t.m0 + i * p.a_rows, za);
           }
           if (kBMn) {
-            load(b, &tm_b, t.n0 + 128 * r, k0, zb);
-            load(b + kGHalf / 2, &tm_b, t.n0 + 128 * r + 64, k0, zb);
+            load(b, tm_b, t.n0 + 128 * r, k0, zb);
+            load(b + kGHalf / 2, tm_b, t.n0 + 128 * r + 64, k0, zb);
           } else if (kEpi == Epi::GateUp) {
             if (kPair) {  // the even CTA holds the gate columns, the odd one the up columns
-              load(b, &tm_b, k0, t.n0, 2 * zb + r);
+              load(b, tm_b, k0, t.n0, 2 * zb + r);
             } else {
-              load(b, &tm_b, k0, t.n0, 2 * zb);
-              load(b + kGHalf / 2, &tm_b, k0, t.n0, 2 * zb + 1);
+              load(b, tm_b, k0, t.n0, 2 * zb);
+              load(b + kGHalf / 2, tm_b, k0, t.n0, 2 * zb + 1);
             }
           } else {
-            load(b, &tm_b, k0, t.n0 + 128 * r, zb);
+            load(b, tm_b, k0, t.n0 + 128 * r, zb);
           }
         }
         __syncwarp();
         if (++s == kStages) { s = 0; ph ^= 1u; }
       }
     }
+    c.s = s;
+    c.ph = ph;
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer
     constexpr uint32_t kIdesc = idesc_f16(tile_m(kPair), kN, kBf16, kAMn, kBMn);
-    int s = 0, acc_it = 0;
-    uint32_t ph = 0;
+    int s = c.s, acc_it = c.acc_it;
+    uint32_t ph = c.ph;
     bool ok = rank == 0;
     bool more = ok && walk.next(&t);
     while (more) {
@@ -462,13 +497,16 @@ __global__ void __launch_bounds__(kGThreads, 1)
       if (!ok) break;
       ++acc_it;
     }
+    c.s = s;
+    c.ph = ph;
+    c.acc_it = acc_it;
   } else if (warp == kGPatchWarp) {
     // ------------------------------------------------ rows behind the routed ones
     // Padding, or another expert's rows, in an expert's last chunk become
     // zeros (a product with zero would keep a NaN), up to the MMA's next 16.
     if (kSched == Sched::Experts) {
-      int count = 0;
-      uint32_t seen = 0;  // parity of part[s], one bit a stage
+      int count = c.count;
+      uint32_t seen = c.seen;  // parity of part[s], one bit a stage
       bool ok = true;
       while (ok && walk.next(&t)) {
         if (t.nk > 0 && ragged(t, t.nk - 1)) {
@@ -496,6 +534,8 @@ __global__ void __launch_bounds__(kGThreads, 1)
         }
         count += t.nk;
       }
+      c.count = count;
+      c.seen = seen;
     }
   } else {
     // ------------------------------------------------ epilogue
@@ -506,7 +546,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
     constexpr int kHalfCols = kN / 2;
     const uint32_t stg0 = smem_u32(smem + kStaging + (warp - 2) * 2 * kBuf);
     uint64_t* side = side_full + (warp - 2) * 2;
-    int piece = 0;  // pieces so far; piece % 2 is the buffer
+    int piece = c.piece;  // pieces so far; piece % 2 is the buffer
     auto buffer = [&] { return stg0 + static_cast<uint32_t>(piece & 1) * kBuf; };
     // 16 bytes of this thread's row of a staging tile, swizzled as its tensor map says
     auto at64 = [&](int tile, int i) { return buffer() + tile * kGTile + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4); };
@@ -572,18 +612,18 @@ __global__ void __launch_bounds__(kGThreads, 1)
           const int row = t.m0 + 32 * q + i * p.store_rows;
           uint8_t* dst = smem + kStaging + (warp - 2) * 2 * kBuf + b * kBuf + i * p.store_rows * 64;
           if (kEpi == Epi::SwigluGrad) {
-            tma_load_3d(dst, &tm_c, &side[b], col, 0, row, pol);
-            tma_load_3d(dst + kGTile, &tm_c, &side[b], col, 1, row, pol);
+            tma_load_3d(dst, tm_c, &side[b], col, 0, row, pol);
+            tma_load_3d(dst + kGTile, tm_c, &side[b], col, 1, row, pol);
           } else {
-            tma_load_3d(dst, &tm_c, &side[b], col, row, t.z, pol);
-            if (kSideTiles == 2) tma_load_3d(dst + kGTile, &tm_c2, &side[b], col, row, t.z, pol);
+            tma_load_3d(dst, tm_c, &side[b], col, row, t.z, pol);
+            if (kSideTiles == 2) tma_load_3d(dst + kGTile, tm_c2, &side[b], col, row, t.z, pol);
           }
         }
       }
       __syncwarp();
     };
-    int acc_it = 0;
-    uint32_t side_ph = 0;  // parity of side[b], a bit each
+    int acc_it = c.acc_it;
+    uint32_t side_ph = c.side_ph;  // parity of side[b], a bit each
     bool ok = true;
     while (ok && walk.next(&t)) {
       if (t.nk == 0 && p.accumulate) continue;
@@ -637,7 +677,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
                 }
                 put(at64(0, i), w[0], w[1], w[2], w[3]);
               }
-              stored([&] { store(&tm_d, 0, col, half, true); });
+              stored([&] { store(tm_d, 0, col, half, true); });
             }
             buffer_free();
 #pragma unroll
@@ -652,7 +692,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
               }
               put(at64(0, i), w[0], w[1], w[2], w[3]);
             }
-            stored([&] { store(&tm_d2, 0, col, 0, false); });
+            stored([&] { store(tm_d2, 0, col, 0, false); });
           }
         } else if (kSide) {
 #pragma unroll 1
@@ -693,8 +733,8 @@ __global__ void __launch_bounds__(kGThreads, 1)
                 put(at64(1, i), ou[0], ou[1], ou[2], ou[3]);
               }
               stored([&] {
-                store(&tm_d, 0, col, 0, true);
-                store(&tm_d, 1, col, 1, true);
+                store(tm_d, 0, col, 0, true);
+                store(tm_d, 1, col, 1, true);
               });
             } else if (kEpi == Epi::Poly) {
               uint32_t w[16];
@@ -721,8 +761,8 @@ __global__ void __launch_bounds__(kGThreads, 1)
               }
               if (t.mirror) put_transposed(1, w);
               stored([&] {
-                store(&tm_d, 0, col, t.z, false);
-                if (t.mirror) tma_store_3d(&tm_d, buffer() + kGTile, t.m0 + 32 * q, col, t.z);
+                store(tm_d, 0, col, t.z, false);
+                if (t.mirror) tma_store_3d(tm_d, buffer() + kGTile, t.m0 + 32 * q, col, t.z);
               });
             } else {
               const float* diag = p.diag + static_cast<int64_t>(t.z) * p.side;
@@ -765,7 +805,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
                     w[j] = pack_b16(y[8 * i + 2 * j] * p.beta, y[8 * i + 2 * j + 1] * p.beta);
                   put(at64(0, i), w[0], w[1], w[2], w[3]);
                 }
-                stored([&] { store(&tm_d, 0, col, t.z, false); });
+                stored([&] { store(tm_d, 0, col, t.z, false); });
               } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -781,8 +821,8 @@ __global__ void __launch_bounds__(kGThreads, 1)
                   put(at64(1, i), wl[0], wl[1], wl[2], wl[3]);
                 }
                 stored([&] {
-                  store(&tm_d, 0, col, t.z, false);
-                  store(&tm_d2, 1, col, t.z, false);
+                  store(tm_d, 0, col, t.z, false);
+                  store(tm_d2, 1, col, t.z, false);
                 });
               }
             }
@@ -803,7 +843,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
                 const int e = 16 * half + 4 * i;
                 put(at64(0, i), v[e], v[e + 1], v[e + 2], v[e + 3]);
               }
-              stored([&] { store(&tm_d, 0, col + 16 * half, t.z, false); });
+              stored([&] { store(tm_d, 0, col + 16 * half, t.z, false); });
             }
           }
         } else if (kEpi == Epi::Gram) {
@@ -819,11 +859,11 @@ __global__ void __launch_bounds__(kGThreads, 1)
             buffer_free();
 #pragma unroll
             for (int i = 0; i < 4; ++i) put(at64(0, i), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-            stored([&] { store(&tm_d, 0, col, t.z, false); });
+            stored([&] { store(tm_d, 0, col, t.z, false); });
             if (t.mirror) {
               buffer_free();
               put_transposed(0, w);
-              stored([&] { tma_store_3d(&tm_d, buffer(), t.m0 + 32 * q, col, t.z); });
+              stored([&] { tma_store_3d(tm_d, buffer(), t.m0 + 32 * q, col, t.z); });
             }
           }
         } else {  // Rows, Weights in bf16
@@ -844,7 +884,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
               }
               put(at64(0, i), w[0], w[1], w[2], w[3]);
             }
-            stored([&] { store(&tm_d, 0, col, kSched == Sched::Blocks ? 0 : t.z, false); });
+            stored([&] { store(tm_d, 0, col, kSched == Sched::Blocks ? 0 : t.z, false); });
           }
         }
         if (!ok) break;
@@ -862,26 +902,43 @@ __global__ void __launch_bounds__(kGThreads, 1)
       }
     }
     if (lane == 0) bulk_wait_all();
+    c.acc_it = acc_it;
+    c.side_ph = side_ph;
+    c.piece = piece;
   }
+}
 
-  __syncwarp();
-  tc_fence_before();
-  __syncthreads();
-  if (*abort_flag) {
-    // copies and MMAs issued before a wait gave up may still be landing; they
-    // finish within microseconds
-    const unsigned long long t0 = globaltimer();
-    while (globaltimer() - t0 < 100000ull) __nanosleep(1000);
+
+template <Form kForm, Sched kSched, Epi kEpi, bool kPair, bool kBf16>
+__global__ void __launch_bounds__(kGThreads, 1)
+    tile_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                     const __grid_constant__ CUtensorMap tm_d, const __grid_constant__ CUtensorMap tm_d2,
+                     const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_c2,
+                     const __grid_constant__ GemmParams p) {
+  constexpr int kStages = gemm_stages(kSched, kEpi), kBuf = gemm_buf(kEpi);
+  extern __shared__ uint8_t smem_raw[];
+  TileCta c;
+  pdl_launch_dependents();
+  tile_cta_setup<kStages, kBuf, kPair>(&c, smem_raw);
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&tm_a);
+    prefetch_tmap(&tm_b);
+    prefetch_tmap(&tm_d);
+    if (epi_side(kEpi)) prefetch_tmap(&tm_c);
   }
-  __syncwarp();
-  if (kPair) cluster_sync();  // neither CTA leaves while the other may still read or signal it
-  if (warp == 1) {
-    tc_fence_after();
-    if (kPair)
-      tmem_dealloc_pair(tbase, kTmemCols);
-    else
-      tmem_dealloc(tbase, kTmemCols);
+  int* first = reinterpret_cast<int*>(c.smem + gemm_ctrl(kSched, kEpi) + kGCtrlBytes);
+  int blocks = 0;
+  if (kSched != Sched::Batch) {  // the plan; these launches are not chained
+    const int n = __ldg(p.ntpp) / p.bm;
+    blocks = n < 0 ? 0 : min(n, p.max_blocks);
+    if (kSched == Sched::Experts) find_segments(p, blocks, first);
   }
+  tile_cta_ready<kPair>(&c);
+  if (kSched == Sched::Batch) pdl_wait();  // what a chained launch before this one wrote is read below
+  const int at = static_cast<int>(blockIdx.x), of = static_cast<int>(gridDim.x);
+  Walk<kSched, kEpi, kPair> walk(p, static_cast<int>(c.rank), kPair ? at / 2 : at, kPair ? of / 2 : of, blocks, first);
+  tile_product<kForm, kSched, kEpi, kPair, kBf16, kStages, kBuf>(c, walk, &tm_a, &tm_b, &tm_d, &tm_d2, &tm_c, &tm_c2, p);
+  tile_cta_leave<kPair>(c);
 }
 
 // ------------------------------------------------------------------ host side
