@@ -163,7 +163,8 @@ static int run_blocks(const ExpertCall& c, int64_t cols, const void* in, int64_t
              : blocks_tiled<kForm, kEpi, false>(c, in, width_in, args...);
 }
 
-// grad[e] (m x n) = sum over e's rows of a^T b, a (capacity, m), b (capacity, n).
+// grad[e] (m x n) = sum over e's rows of a^T b, a (capacity, m), b (capacity, n).  Launched to run beside the rows'
+// gradient before it (which is launched where there is a block): its CTAs take the SMs that run out of tiles there.
 template <bool kPair>
 static int weights_tiled(const ExpertCall& c, const void* a, int64_t m, const void* b, int64_t n, void* grad, int f32,
                          int accumulate) {
@@ -186,7 +187,7 @@ static int weights_tiled(const ExpertCall& c, const void* a, int64_t m, const vo
   if (rc != MOE_OK) return rc;
   t.d2 = t.c = t.c2 = t.d;
   return launch_tile_gemm<Form::TN, Sched::Experts, Epi::Weights, kPair, true>(
-      c.nm, t, p, static_cast<int64_t>(c.E) * p.m_tiles * p.n_tiles, false, c.stream);
+      c.nm, t, p, static_cast<int64_t>(c.E) * p.m_tiles * p.n_tiles, c.capacity / c.bm > 0, c.stream);
 }
 
 static int run_weights(const ExpertCall& c, const void* a, int64_t m, const void* b, int64_t n, void* grad, int f32,

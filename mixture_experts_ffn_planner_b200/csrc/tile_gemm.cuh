@@ -928,7 +928,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
   }
   int* first = reinterpret_cast<int*>(c.smem + gemm_ctrl(kSched, kEpi) + kGCtrlBytes);
   int blocks = 0;
-  if (kSched != Sched::Batch) {  // the plan; these launches are not chained
+  if (kSched != Sched::Batch) {  // the plan, which no launch that this one may overlap has written
     const int n = __ldg(p.ntpp) / p.bm;
     blocks = n < 0 ? 0 : min(n, p.max_blocks);
     if (kSched == Sched::Experts) find_segments(p, blocks, first);
@@ -938,6 +938,9 @@ __global__ void __launch_bounds__(kGThreads, 1)
   const int at = static_cast<int>(blockIdx.x), of = static_cast<int>(gridDim.x);
   Walk<kSched, kEpi, kPair> walk(p, static_cast<int>(c.rank), kPair ? at / 2 : at, kPair ? of / 2 : of, blocks, first);
   tile_product<kForm, kSched, kEpi, kPair, kBf16, kStages, kBuf>(c, walk, &tm_a, &tm_b, &tm_d, &tm_d2, &tm_c, &tm_c2, p);
+  // a weight gradient runs beside the product launched before it, which it does not depend on, but does not end
+  // before it: what follows on the stream waits for both
+  if (kSched == Sched::Experts) pdl_wait();
   tile_cta_leave<kPair>(c);
 }
 
