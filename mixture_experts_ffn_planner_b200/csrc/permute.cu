@@ -26,11 +26,14 @@
 
 namespace moe {
 
-// Threads a block.  With dot products a thread holds a row's vectors of x, y
-// and the products (108 registers): blocks of 128 then fill an SM better (8192
-// tokens of 8 KB, top 8: 199 us, 217 at 256); without, 256 are ahead where
-// there are few tokens (64 tokens of 16 KB: 12 and 16 us).
+// Threads a block.  A gather, and a scatter with dot products, hold many rows'
+// vectors a thread (80 and 108 registers): blocks of 128 then fill an SM
+// better (8192 tokens, top 6, gathered in rows of 8 KB bf16: 78 us, 88 at 256;
+// 3000 tokens in rows of 501 fp32: 18 and 27; 8192 tokens of 8 KB, top 8, with
+// dot products: 199 and 217).  A scatter without them is ahead with 256 (8192
+// tokens of 8 KB, top 8: 118 and 123 us).
 constexpr int kPermThreads = 256;
+constexpr int kPermGatherThreads = 128;
 constexpr int kPermGradThreads = 128;
 constexpr int kPermJ = 8;  // routes handled at once (registers); more routes take another turn
 
@@ -87,7 +90,8 @@ __device__ __forceinline__ void store_vec(T* row, int v, const Vec<T, VB>& x) {
 
 // Vectors of a row that a thread handles at once, a block's width apart: the
 // narrow ones of odd row lengths need several to have as many bytes in flight.
-constexpr int row_unroll(int vb) { return vb == 16 ? 1 : vb == 8 ? 2 : 4; }
+// (Four made no odd length faster, and spilled in bf16: 4000 tokens in rows of 250, 23 us, with two 17.)
+constexpr int row_unroll(int vb) { return vb == 16 ? 1 : 2; }
 
 struct ScatterParams {
   const void* token;           // (T, K): x, or grad_out
@@ -227,11 +231,10 @@ struct GatherParams {
 };
 
 template <typename T, int VB>
-// Three blocks an SM: at two (98 registers) 8192 tokens of 8 KB took 123 us instead of 106.
-__global__ void __launch_bounds__(kPermThreads, 3) row_gather_kernel(const GatherParams p) {
+__global__ void __launch_bounds__(kPermGatherThreads, 6) row_gather_kernel(const GatherParams p) {
   using V = Vec<T, VB>;
   const int nv = p.K / V::n;
-  const int per = kPermThreads / p.tpt;
+  const int per = kPermGatherThreads / p.tpt;
   const int sub = threadIdx.x / p.tpt, tid = threadIdx.x - sub * p.tpt;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * per + sub;
   if (t >= p.T) return;
@@ -321,9 +324,9 @@ static int threads_per_token(int64_t nv, int threads) {
 // Parts that a row is split into, of `span` vectors each: while blocks are
 // fewer than 4 an SM, so that a thread has fewer vectors to wait for in turn
 // (64 tokens of 16 KB, top 8, gathered: 12 -> 8 us).
-static int row_chunks(int64_t blocks, int64_t nv, int tpt, int* span) {
+static int row_chunks(int64_t blocks, int64_t nv, int threads, int tpt, int* span) {
   int64_t n = 1;
-  if (tpt == kPermThreads)
+  if (tpt == threads)
     while (blocks * n < static_cast<int64_t>(std::max(1, sm_count())) * 4 && n * tpt < nv) n <<= 1;
   const int64_t s = ((nv + n - 1) / n + tpt - 1) / tpt * tpt;
   *span = static_cast<int>(s);
@@ -377,7 +380,7 @@ static int run_scatter(const char* nm, ScatterParams p, int dtype, bool grad, cu
   int64_t token_blocks = (static_cast<int64_t>(p.T) + per - 1) / per;
   p.chunks = 1;
   if (!grad) {
-    p.chunks = row_chunks(token_blocks, nv, p.tpt, &p.span);
+    p.chunks = row_chunks(token_blocks, nv, threads, p.tpt, &p.span);
     token_blocks *= p.chunks;
   }
   // The padding goes over all SMs, one place a warp while they last: with 32
@@ -407,12 +410,12 @@ static int run_gather(const char* nm, GatherParams p, int dtype, cudaStream_t s)
     return fail(MOE_ERR_ALIGNMENT, "%s: pointers must be aligned to their element", nm);
   const int vb = vector_bytes(static_cast<int64_t>(p.K) * esize, esize, {p.rows, p.out});
   const int64_t nv = static_cast<int64_t>(p.K) * esize / vb;
-  p.tpt = threads_per_token(nv, kPermThreads);
-  const int per = kPermThreads / p.tpt;
+  p.tpt = threads_per_token(nv, kPermGatherThreads);
+  const int per = kPermGatherThreads / p.tpt;
   const int64_t blocks = (static_cast<int64_t>(p.T) + per - 1) / per;
-  const dim3 grid(static_cast<unsigned>(blocks), row_chunks(blocks, nv, p.tpt, &p.span));
+  const dim3 grid(static_cast<unsigned>(blocks), row_chunks(blocks, nv, kPermGatherThreads, p.tpt, &p.span));
   const cudaError_t err = by_access(dtype, vb, [&](auto tag, auto width) {
-    row_gather_kernel<decltype(tag), decltype(width)::value><<<grid, kPermThreads, 0, s>>>(p);
+    row_gather_kernel<decltype(tag), decltype(width)::value><<<grid, kPermGatherThreads, 0, s>>>(p);
     return cudaGetLastError();
   });
   return err == cudaSuccess ? MOE_OK : cuda_fail(nm, err);
