@@ -177,11 +177,11 @@ struct Walk {
     if (u >= units || u / per_z == z_next) return;
     z_next = u / per_z;
     const int end = first[z_next + 1];
-    const bool any = first[z_next] < end;
-    const int64_t at = static_cast<int64_t>(end - 1) * p.bm;
+    if (first[z_next] == end) return;
+    // (no value is chosen here: that would wait for the loads)
+    const int32_t* block = p.sorted_ids + static_cast<int64_t>(end - 1) * p.bm;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      last_ids[i] = any && 32 * i + lane < p.bm ? __ldg(p.sorted_ids + at + 32 * i + lane) : -1;
+    for (int i = 0; i < 4; ++i) last_ids[i] = __ldg(block + min(32 * i + lane, p.bm - 1));
   }
 
   // The window from block `at` on: a tile begins every tile_m / bm blocks of an expert's run.
@@ -206,15 +206,18 @@ struct Walk {
         before += __popc(heads);
         look(win + 32);
       }
-      const int at = static_cast<int>(__fns(heads, 0, want - before + 1));
+      // the head that has want - before others ahead of it in the window
+      const int ahead = __popc(heads & ((1u << lane) - 1u));
+      const int at = __ffs(static_cast<int>(__ballot_sync(0xffffffffu, (heads >> lane & 1u) && ahead == want - before))) - 1;
       const int b = win + at;
       t->z = __shfl_sync(0xffffffffu, id, at);
       t->n0 = (u - want * p.n_tiles) * kCols;
-      // blocks of the tile: those from b on with its expert
+      // blocks of the tile: those from b on with its expert (id is -1 behind the last), read again where the window ends
       const int per = tile_m(kPair) / p.bm;
-      const uint32_t same = __ballot_sync(
-          0xffffffffu, lane < per && b + lane < blocks && __ldg(p.expert_ids + min(b + lane, blocks - 1)) == t->z);
-      const int run = same == 0xffffffffu ? 32 : __ffs(static_cast<int>(~same)) - 1;
+      uint32_t same = __ballot_sync(0xffffffffu, id == t->z) >> at;
+      if (at + per > 32)
+        same = __ballot_sync(0xffffffffu, b + lane < blocks && __ldg(p.expert_ids + min(b + lane, blocks - 1)) == t->z);
+      const int run = min(per, same == 0xffffffffu ? 32 : __ffs(static_cast<int>(~same)) - 1);
       t->m0 = b * p.bm + rank * 128;
       t->total = run * p.bm;
       t->limit = min(128, t->total - rank * 128);
@@ -248,7 +251,8 @@ struct Walk {
       if (n > 0) {  // whole blocks, and the routed rows that the last one begins with
         t->rows = (n - 1) * p.bm;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) t->rows += __popc(__ballot_sync(0xffffffffu, last_ids[i] >= 0));
+        for (int i = 0; i < 4; ++i)
+          t->rows += __popc(__ballot_sync(0xffffffffu, 32 * i + lane < p.bm && last_ids[i] >= 0));
       }
       t->nk = (t->rows + kGK - 1) / kGK;
       u += stride;
