@@ -91,6 +91,7 @@ class Tuning(ctypes.Structure):
 
 _lock = threading.Lock()
 _lib = None
+_dtypes = {}  # torch's types by short name, once the library is loaded
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -151,6 +152,9 @@ def load(build_if_stale: bool = True) -> ctypes.CDLL:
             fn = getattr(lib, name)
             fn.argtypes = args
             fn.restype = res
+        import torch
+
+        _dtypes.update(i32=torch.int32, f32=torch.float32, bf16=torch.bfloat16)
         _lib = lib
         return lib
 
@@ -628,6 +632,10 @@ def _rows_dtype(t, name):
     raise TypeError(f"{name}: dtype {t.dtype} not in (torch.bfloat16, torch.float32)")
 
 
+def _rows_code(t):
+    return 1 if t.dtype is _dtypes["f32"] else 0
+
+
 def _slots_shape(slots):
     import torch
 
@@ -667,51 +675,83 @@ def moe_route_slots(sorted_token_ids, num_tokens_post_padded, T: int, top_k: int
     return slots
 
 
+def _rows_quick(slots, token, rows, order, weights):
+    """Whether the tensors of a call on rows fit one another, as far as one look tells: True, or False where
+    the checks one by one have to say what is missing or wrong.  token (T, K) and rows (capacity, K) of one
+    type, order None or (sorted_token_ids, num_tokens_post_padded), weights None or (T, top_k).  A call of few
+    tokens is bound by the host, and the checks one by one are a third of it."""
+    try:
+        T, K = token.shape
+        i, capacity, dtype, i32 = slots.get_device(), rows.shape[0], token.dtype, _dtypes["i32"]
+        return (i >= 0 and slots.dtype is i32 and slots.shape[0] == T and slots.dim() == 2 and slots.is_contiguous()
+                and (dtype is _dtypes["bf16"] or dtype is _dtypes["f32"]) and token.get_device() == i
+                and token.is_contiguous() and rows.dtype is dtype and rows.shape == (capacity, K)
+                and rows.get_device() == i and rows.is_contiguous()
+                and (weights is None or (weights.dtype is _dtypes["f32"] and weights.shape == slots.shape
+                                         and weights.get_device() == i and weights.is_contiguous()))
+                and (order is None or (order[0].dtype is i32 and order[0].shape == (capacity,)
+                                       and order[0].get_device() == i and order[0].is_contiguous()
+                                       and order[1].dtype is i32 and order[1].shape == (1,)
+                                       and order[1].get_device() == i)))
+    except (AttributeError, KeyError, ValueError):  # None, before the library is loaded, not two dimensions
+        return False
+
+
 def moe_permute(x, sorted_token_ids, num_tokens_post_padded, slots, out=None, stream=None):
     """Token rows x (T, K), bf16 or fp32, in the planner's order: returns rows (capacity, K) with
     rows[slots[t, j]] = x[t], zeros in padding rows; rows at or past num_tokens_post_padded are not written."""
-    dt = _rows_dtype(x, "x")
-    T, top_k, dev = _slots_shape(slots)
-    K = x.shape[1]
-    _tensor(x, "x", x.dtype, dev, (T, K))
-    capacity = _order(sorted_token_ids, num_tokens_post_padded, dev)
-    if out is None:
-        out = _new((capacity, K), x.dtype, dev, stream)
-    _tensor(out, "out", x.dtype, dev, (capacity, K))
-    _call(load().moe_permute, dev, stream, _ptr(x), dt, _ptr(sorted_token_ids), _ptr(num_tokens_post_padded),
-          _ptr(slots), capacity, T, top_k, K, _ptr(out))
+    if out is None or not _rows_quick(slots, x, out, (sorted_token_ids, num_tokens_post_padded), None):
+        _rows_dtype(x, "x")
+        T, _, dev = _slots_shape(slots)
+        K = x.shape[1]
+        _tensor(x, "x", x.dtype, dev, (T, K))
+        capacity = _order(sorted_token_ids, num_tokens_post_padded, dev)
+        if out is None:
+            out = _new((capacity, K), x.dtype, dev, stream)
+        _tensor(out, "out", x.dtype, dev, (capacity, K))
+    T, top_k = slots.shape
+    capacity, K = out.shape
+    _call(load().moe_permute, slots.device, stream, x.data_ptr(), _rows_code(x), sorted_token_ids.data_ptr(),
+          num_tokens_post_padded.data_ptr(), slots.data_ptr(), capacity, T, top_k, K, out.data_ptr())
     return out
 
 
 def moe_permute_backward(grad_rows, slots, out=None, stream=None):
     """Gradient of moe_permute by x: (T, K), the sum in route order of the rows grad_rows (capacity, K) of a
     token's routes."""
-    dt = _rows_dtype(grad_rows, "grad_rows")
-    T, top_k, dev = _slots_shape(slots)
+    if out is None or not _rows_quick(slots, out, grad_rows, None, None):
+        _rows_dtype(grad_rows, "grad_rows")
+        T, _, dev = _slots_shape(slots)
+        capacity, K = grad_rows.shape
+        _tensor(grad_rows, "grad_rows", grad_rows.dtype, dev, (capacity, K))
+        if out is None:
+            out = _new((T, K), grad_rows.dtype, dev, stream)
+        _tensor(out, "out", grad_rows.dtype, dev, (T, K))
+    T, top_k = slots.shape
     capacity, K = grad_rows.shape
-    _tensor(grad_rows, "grad_rows", grad_rows.dtype, dev, (capacity, K))
-    if out is None:
-        out = _new((T, K), grad_rows.dtype, dev, stream)
-    _tensor(out, "out", grad_rows.dtype, dev, (T, K))
-    _call(load().moe_permute_backward, dev, stream, _ptr(grad_rows), dt, _ptr(slots), capacity, T, top_k, K, _ptr(out))
+    _call(load().moe_permute_backward, slots.device, stream, grad_rows.data_ptr(), _rows_code(grad_rows),
+          slots.data_ptr(), capacity, T, top_k, K, out.data_ptr())
     return out
 
 
 def moe_unpermute(y, slots, topk_weights, out=None, stream=None):
     """out (T, K): per token the sum in route order of topk_weights[t, j] * y[slots[t, j]], y (capacity, K) bf16
     or fp32; fp32 sums, one rounding."""
-    import torch
+    if out is None or topk_weights is None or not _rows_quick(slots, out, y, None, topk_weights):
+        import torch
 
-    dt = _rows_dtype(y, "y")
-    T, top_k, dev = _slots_shape(slots)
+        _rows_dtype(y, "y")
+        T, top_k, dev = _slots_shape(slots)
+        capacity, K = y.shape
+        _tensor(y, "y", y.dtype, dev, (capacity, K))
+        _tensor(topk_weights, "topk_weights", torch.float32, dev, (T, top_k))
+        if out is None:
+            out = _new((T, K), y.dtype, dev, stream)
+        _tensor(out, "out", y.dtype, dev, (T, K))
+    T, top_k = slots.shape
     capacity, K = y.shape
-    _tensor(y, "y", y.dtype, dev, (capacity, K))
-    _tensor(topk_weights, "topk_weights", torch.float32, dev, (T, top_k))
-    if out is None:
-        out = _new((T, K), y.dtype, dev, stream)
-    _tensor(out, "out", y.dtype, dev, (T, K))
-    _call(load().moe_unpermute, dev, stream, _ptr(y), dt, _ptr(slots), _ptr(topk_weights), capacity, T, top_k, K,
-          _ptr(out))
+    _call(load().moe_unpermute, slots.device, stream, y.data_ptr(), _rows_code(y), slots.data_ptr(),
+          topk_weights.data_ptr(), capacity, T, top_k, K, out.data_ptr())
     return out
 
 
@@ -721,7 +761,7 @@ def moe_unpermute_backward(grad_out, y, sorted_token_ids, num_tokens_post_padded
     grad_out[t] and zeros in padding rows, grad_weights (T, top_k) fp32 = <grad_out[t], y[slots[t, j]]>)."""
     import torch
 
-    dt = _rows_dtype(grad_out, "grad_out")
+    _rows_dtype(grad_out, "grad_out")
     T, top_k, dev = _slots_shape(slots)
     K = grad_out.shape[1]
     _tensor(grad_out, "grad_out", grad_out.dtype, dev, (T, K))
@@ -734,9 +774,9 @@ def moe_unpermute_backward(grad_out, y, sorted_token_ids, num_tokens_post_padded
         grad_weights = _new((T, top_k), torch.float32, dev, stream)
     _tensor(grad_y, "grad_y", grad_out.dtype, dev, (capacity, K))
     _tensor(grad_weights, "grad_weights", torch.float32, dev, (T, top_k))
-    _call(load().moe_unpermute_backward, dev, stream, _ptr(grad_out), _ptr(y), dt, _ptr(sorted_token_ids),
-          _ptr(num_tokens_post_padded), _ptr(slots), _ptr(topk_weights), capacity, T, top_k, K, _ptr(grad_y),
-          _ptr(grad_weights))
+    _call(load().moe_unpermute_backward, dev, stream, _ptr(grad_out), _ptr(y), _rows_code(grad_out),
+          _ptr(sorted_token_ids), _ptr(num_tokens_post_padded), _ptr(slots), _ptr(topk_weights), capacity, T, top_k, K,
+          _ptr(grad_y), _ptr(grad_weights))
     return grad_y, grad_weights
 
 
