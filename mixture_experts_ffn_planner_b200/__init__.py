@@ -781,7 +781,7 @@ def moe_unpermute_backward(grad_out, y, sorted_token_ids, num_tokens_post_padded
 
 
 def _expert_plan(w, name, sorted_token_ids, expert_ids, num_tokens_post_padded, block_m):
-    """Device, capacity and the plan's pointers of an expert product, w (E, rows, cols) its weights."""
+    """Device and capacity of an expert product, w (E, rows, cols) its weights."""
     import torch
 
     if w is None:
@@ -799,7 +799,28 @@ def _expert_plan(w, name, sorted_token_ids, expert_ids, num_tokens_post_padded, 
     if expert_ids.numel() < blocks:
         raise ValueError(f"expert_ids must hold ceil(capacity / block_m) = {blocks} entries")
     _tensor(expert_ids, "expert_ids", torch.int32, dev, (expert_ids.numel(),))
-    return dev, capacity, (_ptr(sorted_token_ids), _ptr(expert_ids), _ptr(num_tokens_post_padded))
+    return dev, capacity
+
+
+def _expert_quick(w, sorted_token_ids, expert_ids, num_tokens_post_padded, block_m, *rows):
+    """The same as _rows_quick for an expert product: w (E, rows, cols) and every (tensor, width) of `rows` bf16."""
+    try:
+        i, bf16, i32, capacity = w.get_device(), _dtypes["bf16"], _dtypes["i32"], sorted_token_ids.shape[0]
+        if not (i >= 0 and w.dtype is bf16 and w.dim() == 3 and w.is_contiguous()
+                and sorted_token_ids.dtype is i32 and sorted_token_ids.dim() == 1
+                and sorted_token_ids.get_device() == i and sorted_token_ids.is_contiguous()
+                and block_m > 0 and expert_ids.dtype is i32 and expert_ids.dim() == 1
+                and expert_ids.shape[0] * block_m >= capacity and expert_ids.get_device() == i
+                and expert_ids.is_contiguous()
+                and num_tokens_post_padded.dtype is i32 and num_tokens_post_padded.shape == (1,)
+                and num_tokens_post_padded.get_device() == i):
+            return False
+        for t, width in rows:
+            if not (t.dtype is bf16 and t.shape == (capacity, width) and t.get_device() == i and t.is_contiguous()):
+                return False
+        return True
+    except (AttributeError, KeyError, IndexError):
+        return False
 
 
 def _weight_grad(grad, name, w, accumulate, dev, stream):
@@ -822,36 +843,44 @@ def moe_expert_up(rows, w1, sorted_token_ids, expert_ids, num_tokens_post_padded
                   stream=None):
     """Gate/up product with SwiGLU on rows (capacity, K) in the planner's order, w1 (E, N, K), all bf16: returns
     (h (capacity, N), act (capacity, N/2)) with h = rows . w1[e]^T and act = silu(gate) * up from the unrounded h."""
-    import torch
+    plan = (sorted_token_ids, expert_ids, num_tokens_post_padded)
+    E, N, K = getattr(w1, "shape", ()) if getattr(w1, "ndim", 0) == 3 else (0, 1, 0)
+    if N % 2 or not _expert_quick(w1, *plan, block_m, (rows, K), (h, N), (act, N // 2)):
+        import torch
 
-    bf16 = torch.bfloat16
-    dev, capacity, plan = _expert_plan(w1, "w1", sorted_token_ids, expert_ids, num_tokens_post_padded, block_m)
-    E, N, K = w1.shape
-    if N % 2:
-        raise ValueError(f"N = {N} must be even (gate and up halves)")
-    _tensor(rows, "rows", bf16, dev, (capacity, K))
-    if h is None:
-        h = _new((capacity, N), bf16, dev, stream)
-    if act is None:
-        act = _new((capacity, N // 2), bf16, dev, stream)
-    _tensor(h, "h", bf16, dev, (capacity, N))
-    _tensor(act, "act", bf16, dev, (capacity, N // 2))
-    _call(load().moe_expert_up, dev, stream, _ptr(rows), _ptr(w1), *plan, capacity, K, N, E, block_m, _ptr(h), _ptr(act))
+        bf16 = torch.bfloat16
+        dev, capacity = _expert_plan(w1, "w1", *plan, block_m)
+        E, N, K = w1.shape
+        if N % 2:
+            raise ValueError(f"N = {N} must be even (gate and up halves)")
+        _tensor(rows, "rows", bf16, dev, (capacity, K))
+        if h is None:
+            h = _new((capacity, N), bf16, dev, stream)
+        if act is None:
+            act = _new((capacity, N // 2), bf16, dev, stream)
+        _tensor(h, "h", bf16, dev, (capacity, N))
+        _tensor(act, "act", bf16, dev, (capacity, N // 2))
+    _call(load().moe_expert_up, w1.device, stream, rows.data_ptr(), w1.data_ptr(), *map(_ptr, plan), rows.shape[0], K, N,
+          E, block_m, h.data_ptr(), act.data_ptr())
     return h, act
 
 
 def moe_expert_down(act, w2, sorted_token_ids, expert_ids, num_tokens_post_padded, block_m: int, out=None, stream=None):
     """Down product on act (capacity, N/2), w2 (E, K, N/2), bf16: returns y (capacity, K) = act . w2[e]^T."""
-    import torch
+    plan = (sorted_token_ids, expert_ids, num_tokens_post_padded)
+    E, K, half = getattr(w2, "shape", ()) if getattr(w2, "ndim", 0) == 3 else (0, 0, 0)
+    if not _expert_quick(w2, *plan, block_m, (act, half), (out, K)):
+        import torch
 
-    bf16 = torch.bfloat16
-    dev, capacity, plan = _expert_plan(w2, "w2", sorted_token_ids, expert_ids, num_tokens_post_padded, block_m)
-    E, K, half = w2.shape
-    _tensor(act, "act", bf16, dev, (capacity, half))
-    if out is None:
-        out = _new((capacity, K), bf16, dev, stream)
-    _tensor(out, "out", bf16, dev, (capacity, K))
-    _call(load().moe_expert_down, dev, stream, _ptr(act), _ptr(w2), *plan, capacity, K, 2 * half, E, block_m, _ptr(out))
+        bf16 = torch.bfloat16
+        dev, capacity = _expert_plan(w2, "w2", *plan, block_m)
+        E, K, half = w2.shape
+        _tensor(act, "act", bf16, dev, (capacity, half))
+        if out is None:
+            out = _new((capacity, K), bf16, dev, stream)
+        _tensor(out, "out", bf16, dev, (capacity, K))
+    _call(load().moe_expert_down, w2.device, stream, act.data_ptr(), w2.data_ptr(), *map(_ptr, plan), act.shape[0], K,
+          2 * half, E, block_m, out.data_ptr())
     return out
 
 
@@ -860,20 +889,26 @@ def moe_expert_down_backward(grad_y, h, act, w2, sorted_token_ids, expert_ids, n
     """Gradients of moe_expert_down and of the SwiGLU before it: grad_y (capacity, K), h (capacity, N), act
     (capacity, N/2), w2 (E, K, N/2), bf16.  Returns (grad_h (capacity, N) bf16, grad_w2 (E, K, N/2) bf16, or fp32
     when such a buffer is given, which accumulate=True adds to)."""
-    import torch
+    plan = (sorted_token_ids, expert_ids, num_tokens_post_padded)
+    E, K, half = getattr(w2, "shape", ()) if getattr(w2, "ndim", 0) == 3 else (0, 0, 0)
+    quick = _expert_quick(w2, *plan, block_m, (grad_y, K), (h, 2 * half), (act, half), (grad_h, 2 * half))
+    if not quick:
+        import torch
 
-    bf16 = torch.bfloat16
-    dev, capacity, plan = _expert_plan(w2, "w2", sorted_token_ids, expert_ids, num_tokens_post_padded, block_m)
-    E, K, half = w2.shape
-    _tensor(grad_y, "grad_y", bf16, dev, (capacity, K))
-    _tensor(h, "h", bf16, dev, (capacity, 2 * half))
-    _tensor(act, "act", bf16, dev, (capacity, half))
-    grad_w2, gdt = _weight_grad(grad_w2, "grad_w2", w2, accumulate, dev, stream)
-    if grad_h is None:
-        grad_h = _new((capacity, 2 * half), bf16, dev, stream)
-    _tensor(grad_h, "grad_h", bf16, dev, (capacity, 2 * half))
-    _call(load().moe_expert_down_backward, dev, stream, _ptr(grad_y), _ptr(h), _ptr(act), _ptr(w2), *plan, capacity, K,
-          2 * half, E, block_m, _ptr(grad_h), _ptr(grad_w2), gdt, int(accumulate))
+        bf16 = torch.bfloat16
+        dev, capacity = _expert_plan(w2, "w2", *plan, block_m)
+        E, K, half = w2.shape
+        _tensor(grad_y, "grad_y", bf16, dev, (capacity, K))
+        _tensor(h, "h", bf16, dev, (capacity, 2 * half))
+        _tensor(act, "act", bf16, dev, (capacity, half))
+    grad_w2, gdt = _weight_grad(grad_w2, "grad_w2", w2, accumulate, w2.device, stream)
+    if not quick:
+        if grad_h is None:
+            grad_h = _new((capacity, 2 * half), bf16, dev, stream)
+        _tensor(grad_h, "grad_h", bf16, dev, (capacity, 2 * half))
+    _call(load().moe_expert_down_backward, w2.device, stream, grad_y.data_ptr(), h.data_ptr(), act.data_ptr(),
+          w2.data_ptr(), *map(_ptr, plan), act.shape[0], K, 2 * half, E, block_m, grad_h.data_ptr(), grad_w2.data_ptr(),
+          gdt, int(accumulate))
     return grad_h, grad_w2
 
 
@@ -882,19 +917,25 @@ def moe_expert_up_backward(grad_h, rows, w1, sorted_token_ids, expert_ids, num_t
     """Gradients of the gate/up product: grad_h (capacity, N), rows (capacity, K), w1 (E, N, K), bf16.  Returns
     (grad_rows (capacity, K) bf16, grad_w1 (E, N, K) bf16, or fp32 when such a buffer is given, which
     accumulate=True adds to)."""
-    import torch
+    plan = (sorted_token_ids, expert_ids, num_tokens_post_padded)
+    E, N, K = getattr(w1, "shape", ()) if getattr(w1, "ndim", 0) == 3 else (0, 0, 0)
+    quick = _expert_quick(w1, *plan, block_m, (grad_h, N), (rows, K), (grad_rows, K))
+    if not quick:
+        import torch
 
-    bf16 = torch.bfloat16
-    dev, capacity, plan = _expert_plan(w1, "w1", sorted_token_ids, expert_ids, num_tokens_post_padded, block_m)
-    E, N, K = w1.shape
-    _tensor(grad_h, "grad_h", bf16, dev, (capacity, N))
-    _tensor(rows, "rows", bf16, dev, (capacity, K))
-    grad_w1, gdt = _weight_grad(grad_w1, "grad_w1", w1, accumulate, dev, stream)
-    if grad_rows is None:
-        grad_rows = _new((capacity, K), bf16, dev, stream)
-    _tensor(grad_rows, "grad_rows", bf16, dev, (capacity, K))
-    _call(load().moe_expert_up_backward, dev, stream, _ptr(grad_h), _ptr(rows), _ptr(w1), *plan, capacity, K, N, E,
-          block_m, _ptr(grad_rows), _ptr(grad_w1), gdt, int(accumulate))
+        bf16 = torch.bfloat16
+        dev, capacity = _expert_plan(w1, "w1", *plan, block_m)
+        E, N, K = w1.shape
+        _tensor(grad_h, "grad_h", bf16, dev, (capacity, N))
+        _tensor(rows, "rows", bf16, dev, (capacity, K))
+    grad_w1, gdt = _weight_grad(grad_w1, "grad_w1", w1, accumulate, w1.device, stream)
+    if not quick:
+        if grad_rows is None:
+            grad_rows = _new((capacity, K), bf16, dev, stream)
+        _tensor(grad_rows, "grad_rows", bf16, dev, (capacity, K))
+    _call(load().moe_expert_up_backward, w1.device, stream, grad_h.data_ptr(), rows.data_ptr(), w1.data_ptr(),
+          *map(_ptr, plan), rows.shape[0], K, N, E, block_m, grad_rows.data_ptr(), grad_w1.data_ptr(), gdt,
+          int(accumulate))
     return grad_rows, grad_w1
 
 
