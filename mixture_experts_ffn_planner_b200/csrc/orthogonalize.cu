@@ -144,6 +144,12 @@ __global__ void __launch_bounds__(kNsThreads)
   }
 }
 
+}  // namespace moe
+
+#include "ns_resident.cuh"
+
+namespace moe {
+
 // ------------------------------------------------------- a side of at most 64
 constexpr int kNsSmall = 64;
 constexpr int kNsSmallChunks = 32;  // blocks that share a matrix's G G^T, at most
@@ -715,6 +721,7 @@ extern "C" int moe_orthogonalize(const void* g, int g_dtype, int E, int M, int N
   if (std::min(M, N) <= kNsSmall && std::max(M, N) <= kNsClusterMax)
     return run_ns_cluster(nm, g, f32, E, M, N, steps, a, b, c, eps, out, n.stream);
   if (std::min(M, N) <= kNsSmall) return run_ns_small(nm, g, f32, E, M, N, steps, a, b, c, eps, out, n.ws, n.stream);
+  if (ns_resident_fits(E, M, N)) return run_ns_resident(nm, g, f32, E, M, N, steps, a, b, c, eps, out, n.ws, n.stream);
   const bool al = reinterpret_cast<uintptr_t>(g) % 16 == 0;
   double* part = reinterpret_cast<double*>(n.ws + n.L.part);
   ns_norm_kernel<<<dim3(n.L.chunks, E), kNsThreads, 0, n.stream>>>(g, f32, mn, al && mn % 8 == 0 ? 1 : 0, part);

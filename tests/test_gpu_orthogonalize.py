@@ -88,6 +88,19 @@ def test_short_sides(E, M, N):
     moe.moe_device_status()
 
 
+@pytest.mark.parametrize("E,M,N", [(1, 65, 512), (2, 512, 65), (5, 96, 97), (3, 127, 500), (1, 129, 129), (2, 255, 256),
+                                   (2, 256, 449), (1, 511, 192), (4, 200, 320), (56, 128, 65), (57, 128, 65),
+                                   (1, 256, 513), (1, 257, 512)])
+def test_middle_sides(E, M, N):
+    """One launch for shorter sides of 65 to 256 and few matrices, and the sizes next to where it begins and ends."""
+    import mixture_experts_ffn_planner_b200 as moe
+
+    for kind, dtype in (("lowrank", "bfloat16"), ("decades", "float32")):
+        g = matrices(E, M, N, kind, dtype)
+        check(moe.moe_orthogonalize(g), reference(g))
+    moe.moe_device_status()
+
+
 @pytest.mark.parametrize("E,M,N", [(80, 100, 300), (75, 300, 72), (20, 520, 700), (19, 777, 513)])
 def test_many_matrices(E, M, N):
     """Enough tiles for every pair of SMs, with tails on both sides."""
