@@ -1,14 +1,14 @@
 // Newton-Schulz steps on matrices of a shorter side of 65 to 256 and a longer
-// one of at most 512: one launch, a cluster of up to 8 CTAs a matrix, with one
+// one of at most 512 (1024 for a side up to 128): one launch, a cluster of up to 8 CTAs a matrix, with one
 // barrier of the cluster a step instead of three launches.
 //
-// CTA r of a cluster owns 64 places of the longer side, its share of X, in
+// CTA r of a cluster owns 64 (128) places of the longer side, its share of X, in
 // fp32 registers from the first step to the last.  Only X's fp16 operand is
 // shared: every CTA writes its part of it to memory, S x 64, and after the
 // barrier reads all of it (K-major, whichever way the matrix lies) for
 //   A = X X^T                   every CTA all of it: S x S in TMEM, then fp16 in shared memory
 //   B = b A + c A A             from there, replaced in place
-//   X <- (a + d) X + B X        its own 64 places; d: B's diagonal, from step kNsDiagFrom on
+//   X <- (a + d) X + B X        its own places; d: B's diagonal, from step kNsDiagFrom on
 // Computing A and B 8 times over costs tensor time that nobody else could use
 // (a step of 256 x 256: 2 x 4096 cycles), and saves two exchanges through
 // memory and two barriers.
@@ -23,9 +23,11 @@
 namespace moe {
 
 constexpr int kNrThreads = 256;
-constexpr int kNrSide = 256, kNrCols = 64, kNrMaxCtas = 8;
+constexpr int kNrSide = 256, kNrMaxCtas = 8;
+// Places of the longer side a CTA: as many as its threads' 64 registers hold, or fewer on more CTAs.
+__host__ __device__ constexpr int nr_places(int side, int len) { return side <= 128 && len > 64 * kNrMaxCtas ? 128 : 64; }
 constexpr int kNrMat = 4 * 32768;       // A, then B: blocks of 64 columns, 256 rows of 128 bytes
-constexpr int kNrShare = 256 * 128;     // X's own share as an operand: S rows of 64 places
+constexpr int kNrShare = 256 * 128;     // X's own share as an operand: S rows of 64 places, or two blocks of 128 rows
 constexpr int kNrHalf = 128 * 128;       // 64 places of 128 rows of X
 constexpr int kNrStages = 4;            // of one half each, or 2 of both
 constexpr int kNrTotal = 112;  // CTAs a call
@@ -62,11 +64,12 @@ __global__ void __launch_bounds__(kNrThreads, 1)
   const int S = p.side, halves = S > 128 ? 2 : 1, kblocks = (S + 63) / 64, nk = (p.len + 63) / 64;
   const int group = warp >> 2, half = halves == 2 ? group : 0;
   const int row = half * 128 + 32 * (warp & 3) + lane;
-  const int c0 = halves == 2 ? 0 : 32 * group;  // this thread's places of the CTA's 64: 64, or 32 from c0 on
-  const int pieces = halves;                    // of 32
+  const int places = nr_places(S, p.len);
+  const int pieces = halves * places / 64;              // of 32 places: this thread's, from c0 of the CTA's on
+  const int c0 = halves == 2 ? 0 : places / 2 * group;
   const int stages = kNrStages / halves;
   const int64_t z = blockIdx.y;
-  const int l0 = static_cast<int>(cluster_ctarank()) * kNrCols + c0;
+  const int l0 = static_cast<int>(cluster_ctarank()) * places + c0;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status, p.wait_ns));
   };
@@ -86,17 +89,17 @@ __global__ void __launch_bounds__(kNrThreads, 1)
     tmem_relinquish();
   }
 
-  // The share of G, and the norm over the cluster.  Matrices come and go through `mat`, a row of 64 places a row of X,
+  // The share of G, and the norm over the cluster.  Matrices come and go through `mat`, its places a row of X,
   // so that the lanes' accesses to memory are consecutive whichever way the matrix lies (each thread its own row, one
   // after another: 8 us at 128 x 128, and as much for the result).
-  float(*stage)[kNrCols + 1] = reinterpret_cast<float(*)[kNrCols + 1]>(mat);
+  auto stage = [&](int i, int l) -> float& { return reinterpret_cast<float*>(mat)[i * (places + 1) + l]; };
   // Turn k of a thread: row i_lo + k i_by of X, place l_lo + k l_by of the CTA's.
   const int first = l0 - c0;
   const int wrap = halves == 2 ? 1 : 2;  // turns of 128 rows go to two threads each
-  const int i_lo = p.tall ? static_cast<int>(threadIdx.x) % (128 * halves) : static_cast<int>(threadIdx.x) / kNrCols;
-  const int l_lo = p.tall ? static_cast<int>(threadIdx.x) / (128 * halves) : static_cast<int>(threadIdx.x) % kNrCols;
-  const int i_by = p.tall ? 0 : kNrThreads / kNrCols, l_by = p.tall ? wrap : 0;
-  const int turns = p.tall ? kNrCols / wrap : (S + i_by - 1) / i_by;
+  const int i_lo = p.tall ? static_cast<int>(threadIdx.x) % (128 * halves) : static_cast<int>(threadIdx.x) / places;
+  const int l_lo = p.tall ? static_cast<int>(threadIdx.x) / (128 * halves) : static_cast<int>(threadIdx.x) % places;
+  const int i_by = p.tall ? 0 : kNrThreads / places, l_by = p.tall ? wrap : 0;
+  const int turns = p.tall ? places / wrap : (S + i_by - 1) / i_by;
   const int64_t by_i = p.tall ? 1 : p.len, by_l = p.tall ? S : 1;
   const int64_t base = z * S * p.len + first * by_l;
   auto each_place = [&](auto f) {  // f(row, place of the CTA's, index in memory), sixteen at once
@@ -104,15 +107,15 @@ __global__ void __launch_bounds__(kNrThreads, 1)
 #pragma unroll
       for (int u = 0; u < 16; ++u) {
         const int i = i_lo + (k0 + u) * i_by, l = l_lo + (k0 + u) * l_by;
-        if (i < S && l < kNrCols && first + l < p.len) f(i, l, base + i * by_i + l * by_l);
+        if (i < S && l < places && first + l < p.len) f(i, l, base + i * by_i + l * by_l);
       }
     }
   };
   if (p.f32) {
-    each_place([&](int i, int l, int64_t at) { stage[i][l] = __ldg(static_cast<const float*>(p.g) + at); });
+    each_place([&](int i, int l, int64_t at) { stage(i, l) = __ldg(static_cast<const float*>(p.g) + at); });
   } else {
     each_place([&](int i, int l, int64_t at) {
-      stage[i][l] = __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(p.g) + at));
+      stage(i, l) = __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(p.g) + at));
     });
   }
   __syncthreads();
@@ -122,7 +125,7 @@ __global__ void __launch_bounds__(kNrThreads, 1)
   for (int k = 0; k < 2; ++k)
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
-      x[k][j] = k < pieces && row < S && l0 + 32 * k + j < p.len ? stage[row][c0 + 32 * k + j] : 0.f;
+      x[k][j] = k < pieces && row < S && l0 + 32 * k + j < p.len ? stage(row, c0 + 32 * k + j) : 0.f;
       sum += static_cast<double>(x[k][j]) * static_cast<double>(x[k][j]);
     }
 #pragma unroll
@@ -151,7 +154,7 @@ __global__ void __launch_bounds__(kNrThreads, 1)
 #pragma unroll
     for (int j = 0; j < 32; ++j) x[k][j] *= scale;
 
-  // X's share in fp16: to the next operand in memory, and as the own one in shared memory (64 places a row: MN-major)
+  // X's share in fp16: to the next operand in memory, and as the own one in shared memory (MN-major, 64 places a row)
   auto publish = [&](int buf) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -163,7 +166,7 @@ __global__ void __launch_bounds__(kNrThreads, 1)
         for (int j = 0; j < 4; ++j) w[j] = pack_f16(x[k][8 * i + 2 * j], x[k][8 * i + 2 * j + 1]);
         const uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
         const int chunk = (c0 + 32 * k) / 8 + i;
-        *reinterpret_cast<uint4*>(share + row * 128 + ((chunk ^ (row & 7)) << 4)) = v;
+        *reinterpret_cast<uint4*>(share + (chunk >> 3) * kNrHalf + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)) = v;
         if (row < S) *reinterpret_cast<uint4*>(p.x[buf] + (z * S + row) * p.ldx + l0 + 32 * k + 8 * i) = v;
       }
     }
@@ -327,7 +330,7 @@ __global__ void __launch_bounds__(kNrThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_f16_one(tbase + 256 * h, sdesc_sw128(m + kb * 32768 + h * 16384) + 2 * kk,
-                        sdesc_sw128_mn(own + kb * 8192, 8192) + 128 * kk, idesc_f16(128, kNrCols, false, false, true),
+                        sdesc_sw128_mn(own + kb * 8192, kNrHalf) + 128 * kk, idesc_f16(128, places, false, false, true),
                         (kb | kk) != 0);
       tc_commit_one(acc);
     }
@@ -349,11 +352,11 @@ __global__ void __launch_bounds__(kNrThreads, 1)
     for (int k = 0; k < 2; ++k) {
       if (k >= pieces) break;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) stage[row][c0 + 32 * k + j] = x[k][j] * (1.0f / kNsScale);
+      for (int j = 0; j < 32; ++j) stage(row, c0 + 32 * k + j) = x[k][j] * (1.0f / kNsScale);
     }
   }
   __syncthreads();
-  each_place([&](int i, int l, int64_t at) { p.out[at] = __float2bfloat16_rn(stage[i][l]); });
+  each_place([&](int i, int l, int64_t at) { p.out[at] = __float2bfloat16_rn(stage(i, l)); });
   tc_fence_before();
   __syncthreads();
   if (*abort_flag) {  // copies issued before a wait gave up may still be landing
@@ -370,7 +373,8 @@ __global__ void __launch_bounds__(kNrThreads, 1)
 // Clusters that a GPU has room for at once limit it to few matrices: with more, the chained launches share the SMs better.
 inline bool ns_resident_fits(int E, int M, int N) {
   const int side = M < N ? M : N, len = M < N ? N : M;
-  return side <= kNrSide && len <= kNrMaxCtas * kNrCols && static_cast<int64_t>(E) * ((len + 63) / 64) <= kNrTotal;
+  return side <= kNrSide && len <= kNrMaxCtas * nr_places(side, len) &&
+         static_cast<int64_t>(E) * ((len + nr_places(side, len) - 1) / nr_places(side, len)) <= kNrTotal;
 }
 
 static int run_ns_resident(const char* nm, const void* g, int f32, int E, int M, int N, int steps, float a, float b,
@@ -382,10 +386,11 @@ static int run_ns_resident(const char* nm, const void* g, int f32, int E, int M,
   p.len = M < N ? N : M;
   p.tall = M > N ? 1 : 0;
   p.steps = steps;
-  p.ldx = (p.len + 63) / 64 * 64;
+  p.ldx = (p.len + 127) / 128 * 128;  // whole shares
   p.a = a; p.b = b; p.c = c;
   p.eps = eps;
-  // within the workspace's four buffers of iterates: side * ldx <= 2 len * side as len > 64
+  // within the workspace's four buffers of iterates (len * ns_layout's pitch each, or side * it): two of side * ldx,
+  // ldx < len + 128 and len > 64
   const int64_t bytes = (static_cast<int64_t>(E) * p.side * p.ldx * 2 + 255) / 256 * 256;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.wait_ns = kWaitTimeoutNs;
@@ -399,7 +404,7 @@ static int run_ns_resident(const char* nm, const void* g, int f32, int E, int M,
   }
   cudaError_t err = cudaFuncSetAttribute(ns_resident_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNrSmem);
   if (err != cudaSuccess) return cuda_fail(nm, err);
-  const int ctas = (p.len + 63) / 64;
+  const int places = nr_places(p.side, p.len), ctas = (p.len + places - 1) / places;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = ctas;

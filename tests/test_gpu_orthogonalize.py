@@ -90,7 +90,8 @@ def test_short_sides(E, M, N):
 
 @pytest.mark.parametrize("E,M,N", [(1, 65, 512), (2, 512, 65), (5, 96, 97), (3, 127, 500), (1, 129, 129), (2, 255, 256),
                                    (2, 256, 449), (1, 511, 192), (4, 200, 320), (56, 128, 65), (57, 128, 65),
-                                   (1, 256, 513), (1, 257, 512)])
+                                   (1, 256, 513), (1, 257, 512), (2, 128, 513), (1, 1024, 70), (2, 101, 1000), (1, 128, 1025),
+                                   (14, 90, 700), (15, 90, 1024)])
 def test_middle_sides(E, M, N):
     """One launch for shorter sides of 65 to 256 and few matrices, and the sizes next to where it begins and ends."""
     import mixture_experts_ffn_planner_b200 as moe
