@@ -21,13 +21,19 @@
 // decades.  (Earlier it must not be: B's product with the strong directions
 // has to stay in one matrix product.)
 //
-// A side of at most 64 runs in fp32, without tensor cores (whose fp16 noise the
-// steps may amplify to 1e-2 on matrices of a few rows), as one launch: a
-// cluster of up to 8 CTAs a matrix, each with its share of the longer side in
-// shared memory from the first step to the last.  A step sums G G^T over the
-// cluster through distributed shared memory; everything else is local.
-// Where the longer side does not fit (above 5120) the iteration runs on S x S
-// matrices alone, in 64 bits, with X = Q G,
+// Three ways, by the sides:
+//   up to 64        fp32, without tensor cores (whose fp16 noise the steps may
+//                   amplify to 1e-2 on matrices of a few rows), as one launch:
+//                   a cluster of up to 8 CTAs a matrix, each with its share of
+//                   the longer side in shared memory from the first step to
+//                   the last.  A step sums G G^T over the cluster through
+//                   distributed shared memory; everything else is local.
+//   65 to 256, the longer side at most 512 (1024 up to 128), few matrices:
+//                   one launch on the tensor cores (ns_resident.cuh).
+//   else            three chained launches a step (tile_gemm.cuh), of which the
+//                   first two compute half of their symmetric results.
+// Where the longer side of a matrix of up to 64 rows does not fit (above 5120)
+// the iteration runs on S x S matrices alone, in 64 bits, with X = Q G,
 //   P = a I + b A + c A A,  Q <- P Q,  A <- P A P     from A = G G^T / (|G| + eps)^2, Q = I / (|G| + eps)
 // (|G|_F^2 is the trace of G G^T), in one block a matrix, between one pass over
 // G for G G^T and one for Q G.  That takes 64 bits because G G^T squares G's
@@ -35,8 +41,10 @@
 // amplify as well: in fp32 a 3 x 5 matrix of rank one plus noise came out 6e-4
 // off, and 0.3 where Q stood for its transpose.
 //
-// |G|_F of a larger side is summed in 64 bits.  Every sum has a fixed order.  The launches of a call are
-// chained by programmatic dependent launch.
+// |G|_F is summed in 64 bits.  Every sum has a fixed order.  The launches of a
+// call are chained by programmatic dependent launch.  16 matrices of 2048 x
+// 2048 take 2.48 ms: a step 114 us for A, 112 for B (tensor pipe 72 % busy at
+// 1.58 GHz), 209 for the update, which moves 655 MB beside its product.
 #include <algorithm>
 #include <cmath>
 
@@ -352,8 +360,9 @@ __device__ __forceinline__ void ns_outer32(const NsRow32* x, int n, int i0, int 
 }
 
 // A cluster a matrix; `per` places of the longer side a CTA, lc >= per a
-// multiple of 64.  Bound by fp32 issue: 64 x 64 takes 5 steps of three products
-// of 64^3 at 128 fmas a clock, 17 us; in 64 bits on one CTA it took 139.
+// multiple of 64.  Bound by shared memory's reads for 4 x 4 sums a thread: 64 x
+// 64, 5 steps of three products of 64^3, takes 41 us (17 at 128 fmas a clock);
+// in 64 bits on one CTA it took 139.
 __global__ void __launch_bounds__(kNsThreads)
     ns_cluster_kernel(const NsSide n, int per, int lc, int steps, float a, float b, float c, double eps,
                       __nv_bfloat16* out) {

@@ -11,22 +11,27 @@
 // Tiles.  kPair: two CTAs of a cluster work on one 256 x 256 tile with
 // cta_group::2 MMAs: each loads half of A's rows and half of B's, 32 KB a
 // chunk, and takes half of D's rows out of its own TMEM.  That is 128 flop a
-// byte from L2, where one CTA on a 128 x 256 tile has 85 and, at 8192 tokens
-// on 64 experts (K = N = 2048), took 484 us in isolation and 593 us under the
-// power cap, its tensor pipe 67 % busy waiting for operands.  Otherwise one
-// CTA works on 128 x 128: for experts with too few rows to fill 256, where the
-// weights' bytes bound the call and 148 CTAs stream more of them at once.
+// byte from L2, where one CTA on a 128 x 256 tile has 85.  At 8192 tokens on 64
+// experts (K = N = 2048, cold L2) the gate/up product takes 434 us, one CTA
+// took 484; the tensor pipe is busy 84 % of the time at the 1.44 GHz that the
+// power limit leaves, of which an eighth goes to rows behind an expert's last
+// in 256-row tiles.  Otherwise one CTA works on 128 x 128: for experts with too
+// few rows to fill 256, where the weights' bytes bound the call and 148 CTAs
+// stream more of them at once.
 //
 // One CTA per SM walks the tiles.  Warp 0 copies operand chunks by TMA into a
-// ring of 5 or 6 stages (up, 8192 tokens on 64 experts: 543 us with 3, 485 with
-// 4, 471 with 5), warp 1 (of the even CTA of a pair) issues the MMAs, one
-// lane; warps 2-9 take a finished accumulator out of TMEM (two of them
+// ring of 5 or 6 stages (the same product: 543 us with 3, 485 with 4, 471 with
+// 5, all else as it was then), warp 1 (of the even CTA of a pair) issues the
+// MMAs; warps 2-9 take a finished accumulator out of TMEM (two of them
 // alternate, so the epilogue of a tile runs beside the next tile's MMAs) and
 // store it by TMA from two swizzled staging buffers a warp, 32 columns of bf16
-// at a time.  What an epilogue reads beside the accumulator (h, the iterate, the Gram matrix) is
-// loaded by TMA into the staging buffer that its result then replaces, one
-// piece ahead: read by each thread from its own row, as the accumulator lies,
-// those loads took longer than the product.  Every wait is bounded.
+// at a time.  What an epilogue reads beside the accumulator (h, the iterate,
+// the Gram matrix) is loaded by TMA into the staging buffer that its result
+// then replaces, one piece ahead: read by each thread from its own row, as the
+// accumulator lies, those loads took longer than the product.  The roles' warps
+// stay converged, and one elected lane issues: behind a branch on the lane, an
+// instruction's operands are moved over one by one, and the issue of a chunk's
+// four MMAs took 520 cycles, more than the MMAs.  Every wait is bounded.
 //
 // What a tile is (Sched):
 //   Blocks   rows of one expert (consecutive planner blocks, whatever block_m
@@ -34,8 +39,8 @@
 //   Experts  a part of one expert's weight gradient, contracted over the
 //            expert's rows (where they begin is looked up once, into shared
 //            memory: searched for by every role at every tile, it made tiles of
-//            few rows cost 5.8 us); what lies behind the last routed one in a chunk is
-//            cleared in shared memory by warp 10, whatever it holds;
+//            few rows cost 5.8 us); what lies behind the last routed one in a
+//            chunk is cleared in shared memory by warp 10, whatever it holds;
 //   Batch    a part of one matrix of a batch; of a symmetric one (Gram, Poly)
 //            the tiles on and above the diagonal, each stored as it is and
 //            transposed.
