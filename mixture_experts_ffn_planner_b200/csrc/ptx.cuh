@@ -109,9 +109,17 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
   return ok != 0;
 }
 
-// Arrival on a barrier at a shared::cluster address (cluster_addr).
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// Arrivals on a barrier of the other CTA of a pair, at a shared::cluster address
+// (cluster_addr).  A release at cluster scope waits for all that the thread has
+// under way, 1 to 2 us here, and neither use needs it: an accumulator that has
+// been read is ordered by tcgen05's own fences (relaxed); shared memory that
+// was written for the tensor cores has been handed to the async proxy of its
+// own SM, which reads it there, by fence.proxy.async before the arrival.
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_fenced(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // Waits until the phase with the given parity has completed.  Gives up (and

@@ -257,3 +257,19 @@ def test_repeat_is_bitwise_and_streams_and_graphs():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(captured, first))
+
+
+def test_padding_is_cleared_every_time():
+    """Weight gradients of many experts with ragged ends, NaN in all padding: finite and the same bits, run after run."""
+    import torch
+    import mixture_experts_ffn_planner_b200 as moe
+
+    for T, E, bm, K, N in ((9000, 32, 128, 512, 512), (5000, 100, 16, 264, 144)):  # pairs of CTAs, and single ones
+        c = Case(T, 4, E, bm, K, N, drop=0.05, skip=True, seed=7)
+        gh, rows, w1 = c.rows(N), c.rows(K), c.weights(E, N, K)
+        first = moe.moe_expert_up_backward(gh, rows, w1, *c.plan, bm)
+        assert bool(torch.isfinite(first[1]).all()) and bool(torch.isfinite(first[0][: c.n]).all())
+        for _ in range(40):
+            again = moe.moe_expert_up_backward(gh, rows, w1, *c.plan, bm)
+            assert torch.equal(again[1], first[1]) and torch.equal(again[0][: c.n], first[0][: c.n])
+    moe.moe_device_status()
