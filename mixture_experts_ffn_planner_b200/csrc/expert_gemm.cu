@@ -18,25 +18,25 @@ namespace moe {
 // Pairs of CTAs take tiles of 256 x 256, single ones 128 x 128 with twice the
 // bytes from L2 a flop, but four times as many tiles that end four times as
 // soon.  So pairs are for tiles that are many, filled well and long.  Single
-// and pair, us, on 40 experts: up at K = N = 2048, 84 and 86 with 64 rows an
-// expert, 102 and 96 with 192, 512 and 389 with 1536; down at K = 4096, N = 512
-// (a contraction of 256), 70 and 90 with 384 rows, 213 and 218 with 1536; up at
-// K = 4096, N = 512 on 8 experts, 33 and 37 with 384 rows (32 tiles of pairs).
+// and pair, us, on 40 experts: up at K = N = 2048, 102 and 96 with 192 rows an
+// expert, 512 and 389 with 1536; down at K = 512, N = 1024 (a contraction of
+// 512, 160 tiles), 27 and 31 with 384 rows, 41 and 41 with 768; down at K = 4096,
+// N = 512 (256, but 1280 tiles), 64 and 57 with 384 rows.  On 8 experts: down at
+// K = N = 2048, 25 and 26 with 256 rows; up at K = 4096, N = 1024 (32 tiles), 48
+// and 41 with 256.
 // Where a row's pitch is no multiple of 128 bytes, every 128 of an operand lie
 // in two lines of L2 and the bytes count for more: down at K = 1992, N = 1360,
 // 57 and 51 with 128 rows, 88 and 62 with 256.
-constexpr int64_t kPairTiles = 48;
 static bool pairs_for_rows(int64_t tiles, int64_t rows, int64_t contraction, bool lines) {
-  if (tiles < kPairTiles) return false;
-  if (!lines) return rows >= 128 && rows * contraction >= 80 * 1024;
-  return rows >= 192 && rows * contraction >= (contraction >= 512 ? 128 : 384) * 1024;
+  if (tiles < 32 || rows < (lines ? 192 : 128)) return false;
+  const int64_t least = !lines ? 80 : tiles >= 512 ? 96 : contraction >= 1000 ? 187 : 384;
+  return rows * contraction >= least * 1024;
 }
-// Weight gradients, whose contraction is the rows: up_backward at K = 4096,
-// N = 1024 on 40 experts, 224 and 230 us with 192 rows, 302 and 286 with 384;
-// at K = 1000, N = 992, 93 and 91, 138 and 122.
-static bool pairs_for_weights(int64_t tiles, int64_t rows, bool lines) {
-  return tiles >= kPairTiles && rows >= (lines ? 256 : 192);
-}
+// Weight gradients, whose contraction is the rows, from 24 full tiles on: up_backward
+// at K = 4096, N = 1024 on 40 experts, 167 and 147 us with 64 rows, 218 and 175
+// with 192; down_backward at K = 512, N = 1024 on 8 experts, 20 and 15 with 64
+// (beside the rows' gradient there is room for few CTAs), 44 and 46 with 1536.
+static bool pairs_for_weights(int64_t E, int64_t m, int64_t n) { return E * m * n >= 24 * 65536; }
 
 struct ExpertCall {
   const char* nm;
@@ -192,7 +192,7 @@ static int weights_tiled(const ExpertCall& c, const void* a, int64_t m, const vo
 
 static int run_weights(const ExpertCall& c, const void* a, int64_t m, const void* b, int64_t n, void* grad, int f32,
                        int accumulate) {
-  return pairs_for_weights(c.E * ceil_div(m, 256) * ceil_div(n, 256), mean_rows(c), m % 64 == 0 && n % 64 == 0)
+  return pairs_for_weights(c.E, m, n)
              ? weights_tiled<true>(c, a, m, b, n, grad, f32, accumulate)
              : weights_tiled<false>(c, a, m, b, n, grad, f32, accumulate);
 }
