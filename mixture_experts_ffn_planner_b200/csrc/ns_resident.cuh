@@ -1,6 +1,8 @@
 // Newton-Schulz steps on matrices of a shorter side of 65 to 256 and a longer
-// one of at most 512 (1024 for a side up to 128): one launch, a cluster of up to 8 CTAs a matrix, with one
-// barrier of the cluster a step instead of three launches.
+// one of at most 512 (1024 for a side up to 128): one launch, a cluster of up to
+// 8 CTAs a matrix, with one barrier of the cluster a step instead of three
+// launches (128 x 128: 32 us, 79 launched; 256 x 256: 78 and 87; 28 of them: 83
+// and 107).
 //
 // CTA r of a cluster owns 64 (128) places of the longer side, its share of X, in
 // fp32 registers from the first step to the last.  Only X's fp16 operand is
@@ -9,9 +11,12 @@
 //   A = X X^T                   every CTA all of it: S x S in TMEM, then fp16 in shared memory
 //   B = b A + c A A             from there, replaced in place
 //   X <- (a + d) X + B X        its own places; d: B's diagonal, from step kNsDiagFrom on
-// Computing A and B 8 times over costs tensor time that nobody else could use
-// (a step of 256 x 256: 2 x 4096 cycles), and saves two exchanges through
-// memory and two barriers.
+// Computing A and B on every CTA costs tensor time that nobody else could use
+// (4 thousand cycles each of a step's 24 at 256 x 256, where the barrier and the
+// reads of X take 5 and the three accumulators' ways out of TMEM 9), and saves
+// two exchanges through memory and two barriers.  Two CTAs sharing it, each
+// storing its half of A and B into both, took 96 us at 256 x 256: rows of 16
+// bytes a lane go slowly to another CTA's shared memory.
 //
 // The warps work in turn: warp 0 copies, warp 1 issues the MMAs, and all eight
 // take the accumulators, 32 rows each (warp & 3), either all columns of one of
@@ -102,22 +107,28 @@ __global__ void __launch_bounds__(kNrThreads, 1)
   const int turns = p.tall ? places / wrap : (S + i_by - 1) / i_by;
   const int64_t by_i = p.tall ? 1 : p.len, by_l = p.tall ? S : 1;
   const int64_t base = z * S * p.len + first * by_l;
-  auto each_place = [&](auto f) {  // f(row, place of the CTA's, index in memory), sixteen at once
+  auto row_of = [&](int k) { return i_lo + k * i_by; };
+  auto place_of = [&](int k) { return l_lo + k * l_by; };
+  auto index_of = [&](int i, int l) { return base + i * by_i + l * by_l; };
+  // sixteen at once, from clamped places and without a condition: behind one each, loads are waited for one by one
+  auto take = [&](auto load) {
+#pragma unroll 1
     for (int k0 = 0; k0 < turns; k0 += 16) {
+      float v[16];
+#pragma unroll
+      for (int u = 0; u < 16; ++u)
+        v[u] = load(index_of(min(row_of(k0 + u), S - 1), min(place_of(k0 + u), p.len - 1 - first)));
 #pragma unroll
       for (int u = 0; u < 16; ++u) {
-        const int i = i_lo + (k0 + u) * i_by, l = l_lo + (k0 + u) * l_by;
-        if (i < S && l < places && first + l < p.len) f(i, l, base + i * by_i + l * by_l);
+        const int i = row_of(k0 + u), l = place_of(k0 + u);
+        if (i < S && l < places) stage(i, l) = v[u];
       }
     }
   };
-  if (p.f32) {
-    each_place([&](int i, int l, int64_t at) { stage(i, l) = __ldg(static_cast<const float*>(p.g) + at); });
-  } else {
-    each_place([&](int i, int l, int64_t at) {
-      stage(i, l) = __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(p.g) + at));
-    });
-  }
+  if (p.f32)
+    take([&](int64_t at) { return __ldg(static_cast<const float*>(p.g) + at); });
+  else
+    take([&](int64_t at) { return __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(p.g) + at)); });
   __syncthreads();
   float x[2][32];
   double sum = 0.0;
@@ -356,7 +367,11 @@ __global__ void __launch_bounds__(kNrThreads, 1)
     }
   }
   __syncthreads();
-  each_place([&](int i, int l, int64_t at) { p.out[at] = __float2bfloat16_rn(stage(i, l)); });
+#pragma unroll 4
+  for (int k = 0; k < turns; ++k) {
+    const int i = row_of(k), l = place_of(k);
+    if (i < S && l < places && first + l < p.len) p.out[index_of(i, l)] = __float2bfloat16_rn(stage(i, l));
+  }
   tc_fence_before();
   __syncthreads();
   if (*abort_flag) {  // copies issued before a wait gave up may still be landing

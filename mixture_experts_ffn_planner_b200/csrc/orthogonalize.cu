@@ -361,9 +361,9 @@ __device__ __forceinline__ void ns_outer32(const NsRow32* x, int n, int i0, int 
 
 // A cluster a matrix; `per` places of the longer side a CTA, lc >= per a
 // multiple of 64.  Bound by shared memory's reads for 4 x 4 sums a thread: 64 x
-// 64, 5 steps of three products of 64^3, takes 41 us (17 at 128 fmas a clock);
+// 64, 5 steps of three products of 64^3, takes 38 us (17 at 128 fmas a clock);
 // in 64 bits on one CTA it took 139.
-__global__ void __launch_bounds__(kNsThreads)
+__global__ void __launch_bounds__(kNsThreads, 2)  // two an SM: 16 matrices of 64 x 2000 need 128 CTAs in clusters of 8
     ns_cluster_kernel(const NsSide n, int per, int lc, int steps, float a, float b, float c, double eps,
                       __nv_bfloat16* out) {
   extern __shared__ __align__(16) uint8_t ns_smem[];
@@ -378,13 +378,30 @@ __global__ void __launch_bounds__(kNsThreads)
   const int base = static_cast<int>(rank) * per;
   const int nl = max(0, min(per, n.len - base));  // this CTA's places
   double sum = 0.0;
-  for (int l0 = 0; l0 < lc; l0 += kNsSmall)
-    for (int e = tid; e < kNsSmall * kNsSmall; e += kNsThreads) {
-      const int i = n.i_of(e), l = l0 + n.l_of(e);
-      const float v = i < n.side && l < nl ? ns_load(n.g, n.f32, n.at(z, i, base + l)) : 0.f;
-      X[l][i] = v;
-      sum += static_cast<double>(v) * static_cast<double>(v);
+  // A thread's 16 values of a panel are loaded at once, from a clamped place and without a condition: behind one each,
+  // they were waited for one by one (64 x 2000: 29 thousand cycles).
+  for (int l0 = 0; l0 < lc; l0 += kNsSmall) {
+    constexpr int kTurns = kNsSmall * kNsSmall / kNsThreads;
+    float v[kTurns];
+    auto take = [&](auto load) {
+#pragma unroll
+      for (int k = 0; k < kTurns; ++k) {
+        const int i = n.i_of(tid + k * kNsThreads), l = base + l0 + n.l_of(tid + k * kNsThreads);
+        v[k] = load(n.at(z, min(i, n.side - 1), min(l, n.len - 1)));
+      }
+    };
+    if (n.f32)
+      take([&](int64_t at) { return __ldg(static_cast<const float*>(n.g) + at); });
+    else
+      take([&](int64_t at) { return __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(n.g) + at)); });
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+      const int i = n.i_of(tid + k * kNsThreads), l = l0 + n.l_of(tid + k * kNsThreads);
+      if (i >= n.side || l >= nl) v[k] = 0.f;
+      X[l][i] = v[k];
+      sum += static_cast<double>(v[k]) * static_cast<double>(v[k]);
     }
+  }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
   if ((tid & 31) == 0) warps[tid >> 5] = sum;
@@ -429,12 +446,19 @@ __global__ void __launch_bounds__(kNsThreads)
       const int rows = kNsSmall / static_cast<int>(ranks);
       for (int e = tid; e < rows * (kNsSmall / 4); e += kNsThreads) {
         const int i = static_cast<int>(rank) * rows + e / (kNsSmall / 4), j = e % (kNsSmall / 4) * 4;
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (uint32_t q = 0; q < ranks; ++q) {
-          const float4 v = ld_dsmem4(cluster_addr(&P[i][j], q));
-          s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
-        }
-        for (uint32_t q = 0; q < ranks; ++q) st_dsmem4(cluster_addr(&A[i][j], q), s);
+        float4 v[8];
+#pragma unroll
+        for (uint32_t q = 0; q < 8; ++q)
+          if (q < ranks) v[q] = ld_dsmem4(cluster_addr(&P[i][j], q));
+        float4 s = v[0];
+#pragma unroll
+        for (uint32_t q = 1; q < 8; ++q)
+          if (q < ranks) {
+            s.x += v[q].x; s.y += v[q].y; s.z += v[q].z; s.w += v[q].w;
+          }
+#pragma unroll
+        for (uint32_t q = 0; q < 8; ++q)
+          if (q < ranks) st_dsmem4(cluster_addr(&A[i][j], q), s);
       }
       cluster_sync();
     } else {

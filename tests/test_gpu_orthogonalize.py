@@ -76,7 +76,7 @@ def test_larger_matrices():
         check(moe.moe_orthogonalize(g), reference(g))
 
 
-@pytest.mark.parametrize("E,M,N", [(1, 64, 65), (3, 17, 130), (2, 256, 61), (4, 64, 257), (2, 2, 640), (1, 5120, 64),
+@pytest.mark.parametrize("E,M,N", [(1, 64, 65), (3, 33, 520), (1, 32, 513), (3, 17, 130), (2, 256, 61), (4, 64, 257), (2, 2, 640), (1, 5120, 64), (1, 4608, 31), (1, 64, 4609),
                                    (1, 64, 5121), (2, 63, 9000), (150, 40, 500)])
 def test_short_sides(E, M, N):
     """Every way of a side of at most 64: one CTA a matrix, clusters of 2, 4 and 8, and a side too long for them."""
