@@ -400,11 +400,12 @@ MOE_API int moe_expert_up_backward(const void* grad_h, const void* rows, const v
  *              aligned; needs no initialisation; calls that overlap in time
  *              must not share it.
  * Any E, M, N >= 1 whose tiles of 64 x 64 number fewer than 2^31, E <=
- * 65535; steps >= 1; |a|, |b|, |c| <= 64; eps >= 0.  Matrix operands are held
- * in fp16 with fp32 sums, the iterate in 22 bits: the iterates' entries must
- * stay below 1023 in magnitude (the usual coefficients keep them below 2),
- * and a matrix whose norm is below eps / 1000 loses precision.  A zero matrix
- * gives zeros.
+ * 65535; steps >= 1; |a|, |b|, |c| <= 64; eps >= 0.  Where the shorter side is
+ * above 64, matrix operands are held in fp16 with fp32 sums, the iterate in 22
+ * bits or more: the iterates' entries must stay below 1023 in magnitude (the
+ * usual coefficients keep them below 2), and a matrix whose norm is below eps /
+ * 1000 loses precision.  Shorter sides run in fp32, or in 64 bits where the
+ * longer one is above 5120.  A zero matrix gives zeros (for eps > 0).
  * ---------------------------------------------------------------------- */
 MOE_API int64_t moe_orthogonalize_workspace_bytes(int E, int M, int N);
 MOE_API int moe_orthogonalize(const void* g, int g_dtype, int E, int M, int N, int steps, float a, float b, float c,
