@@ -110,16 +110,16 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
 }
 
 // Arrivals on a barrier of the other CTA of a pair, at a shared::cluster address
-// (cluster_addr).  A release at cluster scope waits for all that the thread has
-// under way, 1 to 2 us here, and neither use needs it: an accumulator that has
-// been read is ordered by tcgen05's own fences (relaxed); shared memory that
-// was written for the tensor cores has been handed to the async proxy of its
-// own SM, which reads it there, by fence.proxy.async before the arrival.
+// (cluster_addr).  Relaxed: for an accumulator that has been read, which
+// tcgen05's own fences order.  Released: for what the thread (and those it has
+// synchronised with) wrote; the scope is named, since an arrival without one
+// releases to its own CTA alone.  It waits for all that the thread has under
+// way, 1 to 2 us behind bulk stores, so epilogues do not use it.
 __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void mbar_arrive_fenced(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void mbar_arrive_release(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // Waits until the phase with the given parity has completed.  Gives up (and

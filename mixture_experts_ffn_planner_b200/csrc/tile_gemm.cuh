@@ -383,9 +383,8 @@ __device__ __forceinline__ void tile_product(TileCta& c, Walk<kSched, kEpi, kPai
     return mbar_wait(bar, parity, abort_flag, p.status, p.wait_ns);
   };
   // a barrier that threads of the other CTA arrive on.  Cluster scope is dear: an acquire of it for every chunk, with
-  // a releasing arrival from the other CTA, made a chunk of 256 x 256 x 64 cost 1.06 us; releasing arrivals once a
-  // tile still cost the weight gradients of tiles of few rows an eighth (up_backward, 4096 tokens skewed over 128
-  // experts: 475 us, 415 without).
+  // a releasing arrival from the other CTA, made a chunk of 256 x 256 x 64 cost 1.06 us.  So it is for the barriers
+  // that need it: an accumulator's, once a tile, and a chunk's whose last rows warp 10 of either CTA has cleared.
   auto wait_cluster = [&](uint64_t* bar, uint32_t parity) {
     return mbar_wait<kPair>(bar, parity, abort_flag, p.status, p.wait_ns);
   };
@@ -538,7 +537,7 @@ __device__ __forceinline__ void tile_product(TileCta& c, Walk<kSched, kEpi, kPai
           __syncwarp();
           if (lane == 0) {
             if (kPair)
-              mbar_arrive_fenced(cluster_addr(&full[s], 0));
+              mbar_arrive_release(cluster_addr(&full[s], 0));
             else
               mbar_arrive(&full[s]);
           }
