@@ -366,7 +366,9 @@ MOE_API int moe_unpermute_backward(const void* grad_out, const void* y, int rows
  *   zeros.  accumulate != 0 (fp32 only) adds to what is there instead.
  *   capacity is the length of sorted_token_ids; expert_ids holds
  *   ceil(capacity / block_m) entries, ascending over the used blocks and with
- *   an expert's routed rows first in its last block, as moe_align writes them.
+ *   an expert's routed rows first in its last block, as moe_align writes them
+ *   (ids in another order: no access leaves the buffers, but the weight
+ *   gradients mean nothing).
  * Constraints: K % 8 == 0, N % 16 == 0, 1 <= E <= 1024, block_m in {16, 32,
  * 64, 128}; row and weight buffers 16-byte aligned, outputs apart from inputs.
  * The kernels' waits are bounded (moe_device_status).

@@ -51,6 +51,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "segments.h"
 
 namespace moe {
 
@@ -141,13 +142,15 @@ struct Tile {
   int rows;    // Experts: its routed rows
 };
 
-// first[e], e <= E: the first of the plan's blocks whose expert is >= e (by all threads; the ids ascend, and
-// what does not stays in range).
+// first[e], e <= E: the first of the plan's blocks whose expert is >= e (by all threads; segments.h).
+// Two blocks have the same entry only where ids do not ascend: both CTAs of a pair take the least all the same.
 __device__ __forceinline__ void find_segments(const GemmParams& p, int blocks, int* first) {
+  for (int e = static_cast<int>(threadIdx.x); e <= p.E; e += kGThreads) first[e] = blocks;
+  __syncthreads();
   for (int b = static_cast<int>(threadIdx.x); b <= blocks; b += kGThreads) {
-    const int lo = b == 0 ? 0 : min(max(__ldg(p.expert_ids + b - 1), 0), p.E) + 1;
-    const int hi = b == blocks ? p.E : min(__ldg(p.expert_ids + b), p.E);
-    for (int e = lo; e <= hi; ++e) first[e] = b;
+    const SegmentEntries s = segment_entries(b, blocks, p.E, b == 0 ? -1 : __ldg(p.expert_ids + b - 1),
+                                             b == blocks ? p.E : __ldg(p.expert_ids + b));
+    for (int e = s.lo; e <= s.hi; ++e) atomicMin(&first[e], b);
   }
 }
 
@@ -182,7 +185,7 @@ struct Walk {
     if (u >= units || u / per_z == z_next) return;
     z_next = u / per_z;
     const int end = first[z_next + 1];
-    if (first[z_next] == end) return;
+    if (segment_blocks(first[z_next], end) <= 0) return;
     // (no value is chosen here: that would wait for the loads)
     const int32_t* block = p.sorted_ids + static_cast<int64_t>(end - 1) * p.bm;
 #pragma unroll
@@ -251,7 +254,7 @@ struct Walk {
     t->nk = p.nk;
     t->p0 = t->rows = 0;
     if (kSched == Sched::Experts) {
-      const int lo = first[t->z], n = first[t->z + 1] - lo;
+      const int lo = first[t->z], n = segment_blocks(lo, first[t->z + 1]);
       t->p0 = lo * p.bm;
       if (n > 0) {  // whole blocks, and the routed rows that the last one begins with
         t->rows = (n - 1) * p.bm;
