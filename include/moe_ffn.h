@@ -402,7 +402,7 @@ MOE_API int moe_expert_up_backward(const void* grad_h, const void* rows, const v
  *              aligned; needs no initialisation; calls that overlap in time
  *              must not share it.
  * Any E, M, N >= 1 whose tiles of 64 x 64 number fewer than 2^31, E <=
- * 65535; steps >= 1; |a|, |b|, |c| <= 64; eps >= 0.  Where the shorter side is
+ * 65535, M, N <= 2^31 - 2048; steps >= 1; |a|, |b|, |c| <= 64; eps >= 0.  Where the shorter side is
  * above 64, matrix operands are held in fp16 with fp32 sums, the iterate in 22
  * bits or more: the iterates' entries must stay below 1023 in magnitude (the
  * usual coefficients keep them below 2), and a matrix whose norm is below eps /

@@ -711,8 +711,12 @@ static int ns_steps(const NsCall& n) {
   return MOE_OK;
 }
 
+// The longer side: ns_small_gram_kernel steps over it by up to kNsSmallChunks * kNsSmall places in 32 bits, the others
+// by less.
+constexpr int kNsLongest = 2147483647 - kNsSmallChunks * kNsSmall + 1;
+
 static bool ns_sizes_ok(int E, int M, int N) {
-  if (E < 1 || M < 1 || N < 1) return false;
+  if (E < 1 || M < 1 || N < 1 || std::max(M, N) > kNsLongest) return false;
   const int64_t tiles = ((int64_t(M) + 63) / 64) * ((int64_t(N) + 63) / 64);
   return E <= 65535 && tiles * E < (int64_t(1) << 31) && int64_t(M) * N < (int64_t(1) << 40);
 }
@@ -736,7 +740,8 @@ extern "C" int moe_orthogonalize(const void* g, int g_dtype, int E, int M, int N
   if (!(std::abs(a) <= 64.0f && std::abs(b) <= 64.0f && std::abs(c) <= 64.0f))
     return fail(MOE_ERR_UNSUPPORTED, "%s: coefficients must be within [-64, 64]", nm);
   if (E == 0 || M == 0 || N == 0) return MOE_OK;
-  if (!ns_sizes_ok(E, M, N)) return fail(MOE_ERR_UNSUPPORTED, "%s: too many tiles", nm);
+  if (!ns_sizes_ok(E, M, N))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: too many tiles or a side above 2^31 - 2048", nm);
   if (!g || !out || !workspace) return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", nm);
   const int esize = g_dtype == MOE_ROWS_FP32 ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(g) % esize || reinterpret_cast<uintptr_t>(out) % 2 ||
