@@ -70,21 +70,27 @@ struct Vec {
   __device__ __forceinline__ void set(int i, float v) { reinterpret_cast<T*>(&raw)[i] = from_f32<T>(v); }
 };
 
+// Counts a row's vectors.  An index or an end of a part may lie beyond the row by up to half of it, or by a turn of the
+// block: past 2^31 where a row of nearly that many elements is accessed one by one.  (Unsigned for all widths costs
+// the gathers of 8-byte vectors a tenth: 8192 tokens of 1004 bf16, top 8, 33 us, unsigned 37.)
 template <typename T, int VB>
-__device__ __forceinline__ Vec<T, VB> load_vec(const T* row, int v) {
+using RowIndex = std::conditional_t<VB == sizeof(T), uint32_t, int>;
+
+template <typename T, int VB>
+__device__ __forceinline__ Vec<T, VB> load_vec(const T* row, RowIndex<T, VB> v) {
   Vec<T, VB> r;
   r.raw = __ldg(reinterpret_cast<const typename Raw<VB>::type*>(row) + v);
   return r;
 }
 // The same for what nothing reads again (8192 tokens of 8 KB gathered: 104.5 us, 106.5 without the hint).
 template <typename T, int VB>
-__device__ __forceinline__ Vec<T, VB> load_vec_once(const T* row, int v) {
+__device__ __forceinline__ Vec<T, VB> load_vec_once(const T* row, RowIndex<T, VB> v) {
   Vec<T, VB> r;
   r.raw = __ldcs(reinterpret_cast<const typename Raw<VB>::type*>(row) + v);
   return r;
 }
 template <typename T, int VB>
-__device__ __forceinline__ void store_vec(T* row, int v, const Vec<T, VB>& x) {
+__device__ __forceinline__ void store_vec(T* row, RowIndex<T, VB> v, const Vec<T, VB>& x) {
   reinterpret_cast<typename Raw<VB>::type*>(row)[v] = x.raw;
 }
 
@@ -103,7 +109,8 @@ struct ScatterParams {
   void* row_out;               // (capacity, K)
   float* grad_w;               // (T, top_k), or null
   int64_t capacity;
-  int T, top_k, K, tpt, chunks, span, pad_blocks, pad_step;
+  int T, top_k, K, tpt, chunks, pad_blocks, pad_step;
+  uint32_t span;
 };
 
 // Blocks [0, pad_blocks) write zeros into the padding rows below the padded
@@ -111,9 +118,11 @@ struct ScatterParams {
 // of `chunks` parts (span vectors) of a token's row.
 template <typename T, int VB, bool kGrad>
 __global__ void __launch_bounds__(kGrad ? kPermGradThreads : kPermThreads) row_scatter_kernel(const ScatterParams p) {
-  constexpr int kThreads = kGrad ? kPermGradThreads : kPermThreads, kU = row_unroll(VB);
+  constexpr int kThreads = kGrad ? kPermGradThreads : kPermThreads;
+  constexpr int kU = row_unroll(VB);
   using V = Vec<T, VB>;
-  const int nv = p.K / V::n;
+  using Ix = RowIndex<T, VB>;
+  const Ix nv = p.K / V::n, tpt = p.tpt;
   const int64_t R = static_cast<int64_t>(p.T) * p.top_k;
   if (static_cast<int>(blockIdx.x) < p.pad_blocks) {
     // one warp looks at pad_step (at most 32) places at a time and clears the rows of those that hold no route
@@ -132,7 +141,7 @@ __global__ void __launch_bounds__(kGrad ? kPermGradThreads : kPermThreads) row_s
       for (int i = 0; i < V::n; ++i) zero.set(i, 0.f);
       for (uint32_t m = __ballot_sync(0xffffffffu, pad); m; m &= m - 1) {
         T* row = static_cast<T*>(p.row_out) + (p0 + __ffs(static_cast<int>(m)) - 1) * p.K;
-        for (int v = lane; v < nv; v += 32) store_vec<T, VB>(row, v, zero);
+        for (Ix v = lane; v < nv; v += 32) store_vec<T, VB>(row, v, zero);
       }
     }
     return;
@@ -142,7 +151,8 @@ __global__ void __launch_bounds__(kGrad ? kPermGradThreads : kPermThreads) row_s
   const int sub = threadIdx.x / p.tpt, tid = threadIdx.x - sub * p.tpt;
   const uint32_t place = blockIdx.x - static_cast<uint32_t>(p.pad_blocks), chunks = static_cast<uint32_t>(p.chunks);
   const int64_t t = static_cast<int64_t>(kGrad ? place : place / chunks) * per + sub;  // a dot product takes the whole row
-  const int v_lo = kGrad ? 0 : static_cast<int>(place % chunks) * p.span, v_hi = kGrad ? nv : min(nv, v_lo + p.span);
+  const Ix span = static_cast<Ix>(p.span), v_lo = kGrad ? 0 : static_cast<Ix>(place % chunks) * span;
+  const Ix v_hi = kGrad ? nv : min(nv, v_lo + span);
   const bool live = t < p.T;
   const T* src = static_cast<const T*>(p.token) + t * p.K;
   for (int j0 = 0; j0 < p.top_k; j0 += kPermJ) {
@@ -160,22 +170,22 @@ __global__ void __launch_bounds__(kGrad ? kPermGradThreads : kPermThreads) row_s
       at[j] = s >= 0 && s < p.capacity ? static_cast<int64_t>(s) * p.K : -1;
     }
     if (live) {
-      for (int v0 = v_lo + tid; v0 < v_hi; v0 += kU * p.tpt) {
+      for (Ix v0 = v_lo + tid; v0 < v_hi; v0 += kU * tpt) {
         V x[kU];
 #pragma unroll
         for (int u = 0; u < kU; ++u)
-          if (u == 0 || v0 + u * p.tpt < v_hi) x[u] = load_vec<T, VB>(src, v0 + u * p.tpt);
+          if (u == 0 || v0 + u * tpt < v_hi) x[u] = load_vec<T, VB>(src, v0 + u * tpt);
         if (kGrad) {
           V y[kU][kPermJ];
 #pragma unroll
           for (int u = 0; u < kU; ++u)
 #pragma unroll
             for (int j = 0; j < kPermJ; ++j)
-              if (at[j] >= 0 && (u == 0 || v0 + u * p.tpt < v_hi))
-                y[u][j] = load_vec<T, VB>(static_cast<const T*>(p.rows) + at[j], v0 + u * p.tpt);
+              if (at[j] >= 0 && (u == 0 || v0 + u * tpt < v_hi))
+                y[u][j] = load_vec<T, VB>(static_cast<const T*>(p.rows) + at[j], v0 + u * tpt);
 #pragma unroll
           for (int u = 0; u < kU; ++u) {
-            if (u > 0 && v0 + u * p.tpt >= v_hi) break;
+            if (u > 0 && v0 + u * tpt >= v_hi) break;
 #pragma unroll
             for (int j = 0; j < kPermJ; ++j) {
               if (at[j] < 0) continue;
@@ -185,16 +195,16 @@ __global__ void __launch_bounds__(kGrad ? kPermGradThreads : kPermThreads) row_s
                 dot[j] = fmaf(x[u].get(i), y[u][j].get(i), dot[j]);
                 g.set(i, w[j] * x[u].get(i));
               }
-              store_vec<T, VB>(static_cast<T*>(p.row_out) + at[j], v0 + u * p.tpt, g);
+              store_vec<T, VB>(static_cast<T*>(p.row_out) + at[j], v0 + u * tpt, g);
             }
           }
         } else {
 #pragma unroll
           for (int u = 0; u < kU; ++u) {
-            if (u > 0 && v0 + u * p.tpt >= v_hi) break;
+            if (u > 0 && v0 + u * tpt >= v_hi) break;
 #pragma unroll
             for (int j = 0; j < kPermJ; ++j)
-              if (at[j] >= 0) store_vec<T, VB>(static_cast<T*>(p.row_out) + at[j], v0 + u * p.tpt, x[u]);
+              if (at[j] >= 0) store_vec<T, VB>(static_cast<T*>(p.row_out) + at[j], v0 + u * tpt, x[u]);
           }
         }
       }
@@ -227,18 +237,20 @@ struct GatherParams {
   const float* weights;  // (T, top_k), or null
   void* out;             // (T, K)
   int64_t n_rows;
-  int T, top_k, K, tpt, span;
+  int T, top_k, K, tpt;
+  uint32_t span;
 };
 
 template <typename T, int VB>
 __global__ void __launch_bounds__(kPermGatherThreads, 6) row_gather_kernel(const GatherParams p) {
   using V = Vec<T, VB>;
-  const int nv = p.K / V::n;
+  using Ix = RowIndex<T, VB>;
+  const Ix nv = p.K / V::n, tpt = p.tpt;
   const int per = kPermGatherThreads / p.tpt;
   const int sub = threadIdx.x / p.tpt, tid = threadIdx.x - sub * p.tpt;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * per + sub;
   if (t >= p.T) return;
-  const int v_lo = static_cast<int>(blockIdx.y) * p.span, v_hi = min(nv, v_lo + p.span);
+  const Ix span = static_cast<Ix>(p.span), v_lo = static_cast<Ix>(blockIdx.y) * span, v_hi = min(nv, v_lo + span);
   const T* rows = static_cast<const T*>(p.rows);
   T* out = static_cast<T*>(p.out) + t * p.K;
   int64_t at[kPermJ];
@@ -257,7 +269,7 @@ __global__ void __launch_bounds__(kPermGatherThreads, 6) row_gather_kernel(const
   };
   slots_of(0);
   constexpr int kU = row_unroll(VB);
-  for (int v0 = v_lo + tid; v0 < v_hi; v0 += kU * p.tpt) {
+  for (Ix v0 = v_lo + tid; v0 < v_hi; v0 += kU * tpt) {
     float acc[kU][V::n];
 #pragma unroll
     for (int u = 0; u < kU; ++u)
@@ -270,10 +282,10 @@ __global__ void __launch_bounds__(kPermGatherThreads, 6) row_gather_kernel(const
       for (int u = 0; u < kU; ++u)
 #pragma unroll
         for (int j = 0; j < kPermJ; ++j)
-          if (at[j] >= 0 && (u == 0 || v0 + u * p.tpt < v_hi)) y[u][j] = load_vec_once<T, VB>(rows + at[j], v0 + u * p.tpt);
+          if (at[j] >= 0 && (u == 0 || v0 + u * tpt < v_hi)) y[u][j] = load_vec_once<T, VB>(rows + at[j], v0 + u * tpt);
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        if (u > 0 && v0 + u * p.tpt >= v_hi) break;
+        if (u > 0 && v0 + u * tpt >= v_hi) break;
 #pragma unroll
         for (int j = 0; j < kPermJ; ++j) {
           if (at[j] < 0) continue;
@@ -284,11 +296,11 @@ __global__ void __launch_bounds__(kPermGatherThreads, 6) row_gather_kernel(const
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      if (u > 0 && v0 + u * p.tpt >= v_hi) break;
+      if (u > 0 && v0 + u * tpt >= v_hi) break;
       V o;
 #pragma unroll
       for (int i = 0; i < V::n; ++i) o.set(i, acc[u][i]);
-      store_vec<T, VB>(out, v0 + u * p.tpt, o);
+      store_vec<T, VB>(out, v0 + u * tpt, o);
     }
   }
 }
@@ -324,12 +336,12 @@ static int threads_per_token(int64_t nv, int threads) {
 // Parts that a row is split into, of `span` vectors each: while blocks are
 // fewer than 4 an SM, so that a thread has fewer vectors to wait for in turn
 // (64 tokens of 16 KB, top 8, gathered: 12 -> 8 us).
-static int row_chunks(int64_t blocks, int64_t nv, int threads, int tpt, int* span) {
+static int row_chunks(int64_t blocks, int64_t nv, int threads, int tpt, uint32_t* span) {
   int64_t n = 1;
   if (tpt == threads)
     while (blocks * n < static_cast<int64_t>(std::max(1, sm_count())) * 4 && n * tpt < nv) n <<= 1;
   const int64_t s = ((nv + n - 1) / n + tpt - 1) / tpt * tpt;
-  *span = static_cast<int>(s);
+  *span = static_cast<uint32_t>(s);
   return static_cast<int>((nv + s - 1) / s);
 }
 
