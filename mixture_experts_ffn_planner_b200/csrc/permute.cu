@@ -444,6 +444,8 @@ extern "C" int moe_route_slots(const int32_t* sorted_token_ids, const int32_t* n
   if (T == 0) return MOE_OK;
   if (!slots || !num_tokens_post_padded || (capacity > 0 && !sorted_token_ids))
     return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", nm);
+  if (misaligned({sorted_token_ids, num_tokens_post_padded, slots}, 4))
+    return fail(MOE_ERR_ALIGNMENT, "%s: pointers must be aligned to their element", nm);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int64_t R = static_cast<int64_t>(T) * top_k;
   const cudaError_t err = cudaMemsetAsync(slots, 0xFF, static_cast<size_t>(R) * sizeof(int32_t), s);
