@@ -159,11 +159,11 @@ __global__ void __launch_bounds__(kNrThreads, 1)
     asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(cluster_addr(&norm2, q)) : "memory");
     total += v;
   }
-  const float scale = static_cast<float>(static_cast<double>(kNsScale) / (sqrt(total) + p.eps));
+  const NsFactors scale = ns_factors(sqrt(total) + p.eps);
 #pragma unroll
   for (int k = 0; k < 2; ++k)
 #pragma unroll
-    for (int j = 0; j < 32; ++j) x[k][j] *= scale;
+    for (int j = 0; j < 32; ++j) x[k][j] = x[k][j] * scale.pre * scale.post;
 
   // X's share in fp16: to the next operand in memory, and as the own one in shared memory (MN-major, 64 places a row)
   auto publish = [&](int buf) {

@@ -86,6 +86,18 @@ __device__ __forceinline__ void ns_load8(const void* g, int f32, int64_t i, int 
   }
 }
 
+// kNsScale / norm (norm: |G| + eps) as two factors, x = (g * pre) * post.  Below 1.9e-37 it is beyond fp32; pre is then
+// 2^100, which takes subnormals into range without rounding, and 1 otherwise.
+struct NsFactors {
+  float pre, post;
+};
+__device__ __forceinline__ NsFactors ns_factors(double norm) {
+  constexpr double kPre = 1267650600228229401496703205376.0;  // 2^100
+  const double f = static_cast<double>(kNsScale) / norm;
+  const bool tiny = f > 1e18;
+  return {tiny ? static_cast<float>(kPre) : 1.0f, static_cast<float>(tiny ? f / kPre : f)};
+}
+
 // part[z][chunk] = sum of squares over the chunk's share of matrix z.
 __global__ void __launch_bounds__(kNsThreads)
     ns_norm_kernel(const void* __restrict__ g, int f32, int64_t mn, int vec, double* __restrict__ part) {
@@ -118,17 +130,17 @@ __global__ void __launch_bounds__(kNsThreads)
                    double eps, __half* __restrict__ hi, __half* __restrict__ lo) {
   pdl_launch_dependents();
   pdl_wait();  // the partial sums
-  __shared__ float shared_scale;
+  __shared__ NsFactors shared_scale;
   if (threadIdx.x < 32) {  // one warp a block: by every thread, one after another, the sums took 1.7 of 1.8 ms at 16 x 2048^2
     double s = 0.0;
     for (int c = static_cast<int>(threadIdx.x); c < chunks; c += 32)
       s += __ldcg(part + static_cast<int64_t>(blockIdx.y) * chunks + c);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    if (threadIdx.x == 0) shared_scale = static_cast<float>(static_cast<double>(kNsScale) / (sqrt(s) + eps));
+    if (threadIdx.x == 0) shared_scale = ns_factors(sqrt(s) + eps);
   }
   __syncthreads();
-  const float scale = shared_scale;
+  const NsFactors scale = shared_scale;
   const int per_row = ld / 8;
   const int64_t groups = static_cast<int64_t>(M) * per_row;
   const int64_t z = blockIdx.y;
@@ -141,7 +153,7 @@ __global__ void __launch_bounds__(kNsThreads)
     uint32_t wh[4], wl[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float x0 = v[2 * j] * scale, x1 = v[2 * j + 1] * scale;
+      const float x0 = v[2 * j] * scale.pre * scale.post, x1 = v[2 * j + 1] * scale.pre * scale.post;
       wh[j] = pack_f16(x0, x1);
       const float2 h = unpack_f16(wh[j]);
       wl[j] = pack_f16((x0 - h.x) * kLoScale, (x1 - h.y) * kLoScale);
