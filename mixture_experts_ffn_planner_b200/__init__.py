@@ -693,7 +693,7 @@ def _rows_quick(slots, token, rows, order, weights):
                                        and order[0].get_device() == i and order[0].is_contiguous()
                                        and order[1].dtype is i32 and order[1].shape == (1,)
                                        and order[1].get_device() == i)))
-    except (AttributeError, KeyError, ValueError):  # None, before the library is loaded, not two dimensions
+    except (AttributeError, KeyError, IndexError, ValueError):  # None, before the library is loaded, other dimensions
         return False
 
 
