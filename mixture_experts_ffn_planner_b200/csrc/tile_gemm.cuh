@@ -276,8 +276,7 @@ struct Walk {
 // routed rows: from row `rem` of 64 on; 64 or more: nothing.
 __device__ __forceinline__ bool ragged(const Tile& t, int kc) { return t.rows - kc * kGK < kGK; }
 
-// A thread's view of its CTA: the shared memory's parts, and where its warp's
-// role stands in the rings, which go on from one product to the next.
+// A thread's view of its CTA: the shared memory's parts and its place.
 struct TileCta {
   uint8_t* smem;
   uint64_t *full, *empty;
@@ -288,8 +287,6 @@ struct TileCta {
   volatile int* abort_flag;
   int warp, lane;
   uint32_t rank, tbase;
-  int s, acc_it, piece, count;
-  uint32_t ph, side_ph, seen;
 };
 
 // Shared memory's layout, barriers, TMEM; the CTA's other set-up may follow before tile_cta_ready.
@@ -308,8 +305,6 @@ __device__ __forceinline__ void tile_cta_setup(TileCta* c, uint8_t* smem_raw) {
   c->warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   c->lane = threadIdx.x & 31;
   c->rank = kPair ? cluster_ctarank() : 0u;
-  c->s = c->acc_it = c->piece = c->count = 0;
-  c->ph = c->side_ph = c->seen = 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       // pair: the even CTA's twice, for the copies of both, or warp 10 of each
@@ -365,9 +360,9 @@ __device__ __forceinline__ void tile_cta_leave(const TileCta& c) {
   }
 }
 
-// One product: every warp in its role over the tiles of `walk`.
+// The product: every warp in its role over the tiles of `walk`.
 template <Form kForm, Sched kSched, Epi kEpi, bool kPair, bool kBf16, int kStages, int kBuf>
-__device__ __forceinline__ void tile_product(TileCta& c, Walk<kSched, kEpi, kPair>& walk, const CUtensorMap* tm_a,
+__device__ __forceinline__ void tile_product(const TileCta& c, Walk<kSched, kEpi, kPair>& walk, const CUtensorMap* tm_a,
                                              const CUtensorMap* tm_b, const CUtensorMap* tm_d, const CUtensorMap* tm_d2,
                                              const CUtensorMap* tm_c, const CUtensorMap* tm_c2, const GemmParams& p) {
   constexpr int kN = tile_n(kPair);
@@ -396,8 +391,8 @@ __device__ __forceinline__ void tile_product(TileCta& c, Walk<kSched, kEpi, kPai
   if (warp == 0) {
     // ------------------------------------------------ TMA producer
     const uint64_t pol = policy_evict_normal();
-    int s = c.s;
-    uint32_t ph = c.ph;
+    int s = 0;
+    uint32_t ph = 0;
     bool ok = true;
     while (ok && walk.next(&t)) {
       const int za = kSched == Sched::Batch ? t.z : 0;
@@ -452,13 +447,11 @@ __device__ __forceinline__ void tile_product(TileCta& c, Walk<kSched, kEpi, kPai
         if (++s == kStages) { s = 0; ph ^= 1u; }
       }
     }
-    c.s = s;
-    c.ph = ph;
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer
     constexpr uint32_t kIdesc = idesc_f16(tile_m(kPair), kN, kBf16, kAMn, kBMn);
-    int s = c.s, acc_it = c.acc_it;
-    uint32_t ph = c.ph;
+    int s = 0, acc_it = 0;
+    uint32_t ph = 0;
     bool ok = rank == 0;
     bool more = ok && walk.next(&t);
     while (more) {
@@ -510,16 +503,13 @@ __device__ __forceinline__ void tile_product(TileCta& c, Walk<kSched, kEpi, kPai
       if (!ok) break;
       ++acc_it;
     }
-    c.s = s;
-    c.ph = ph;
-    c.acc_it = acc_it;
   } else if (warp == kGPatchWarp) {
     // ------------------------------------------------ rows behind the routed ones
     // Padding, or another expert's rows, in an expert's last chunk become
     // zeros (a product with zero would keep a NaN), up to the MMA's next 16.
     if (kSched == Sched::Experts) {
-      int count = c.count;
-      uint32_t seen = c.seen;  // parity of part[s], one bit a stage
+      int count = 0;      // chunks so far
+      uint32_t seen = 0;  // parity of part[s], one bit a stage
       bool ok = true;
       while (ok && walk.next(&t)) {
         if (t.nk > 0 && ragged(t, t.nk - 1)) {
@@ -547,8 +537,6 @@ __device__ __forceinline__ void tile_product(TileCta& c, Walk<kSched, kEpi, kPai
         }
         count += t.nk;
       }
-      c.count = count;
-      c.seen = seen;
     }
   } else {
     // ------------------------------------------------ epilogue
@@ -559,7 +547,7 @@ __device__ __forceinline__ void tile_product(TileCta& c, Walk<kSched, kEpi, kPai
     constexpr int kHalfCols = kN / 2;
     const uint32_t stg0 = smem_u32(smem + kStaging + (warp - 2) * 2 * kBuf);
     uint64_t* side = side_full + (warp - 2) * 2;
-    int piece = c.piece;  // pieces so far; piece % 2 is the buffer
+    int piece = 0;  // pieces so far; piece % 2 is the buffer
     auto buffer = [&] { return stg0 + static_cast<uint32_t>(piece & 1) * kBuf; };
     // 16 bytes of this thread's row of a staging tile, swizzled as its tensor map says
     auto at64 = [&](int tile, int i) { return buffer() + tile * kGTile + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4); };
@@ -635,8 +623,8 @@ __device__ __forceinline__ void tile_product(TileCta& c, Walk<kSched, kEpi, kPai
       }
       __syncwarp();
     };
-    int acc_it = c.acc_it;
-    uint32_t side_ph = c.side_ph;  // parity of side[b], a bit each
+    int acc_it = 0;
+    uint32_t side_ph = 0;  // parity of side[b], a bit each
     bool ok = true;
     while (ok && walk.next(&t)) {
       if (t.nk == 0 && p.accumulate) continue;
@@ -915,9 +903,6 @@ __device__ __forceinline__ void tile_product(TileCta& c, Walk<kSched, kEpi, kPai
       }
     }
     if (lane == 0) bulk_wait_all();
-    c.acc_it = acc_it;
-    c.side_ph = side_ph;
-    c.piece = piece;
   }
 }
 
