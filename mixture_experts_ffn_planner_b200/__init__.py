@@ -33,6 +33,11 @@ Entry points (same names as the C ABI):
   experts' products on those rows and the gradients by rows and by weights.
 * ``moe_orthogonalize`` -- the experts' weight update made nearly orthogonal
   by Newton-Schulz steps.
+
+The training calls (from ``moe_route_slots`` on) are plain functions on tensors:
+autograd records none of them, and their results require no gradient, whatever
+their inputs do.  A gradient is what the ``_backward`` call returns; a layer in
+an autograd graph wraps each pair in a ``torch.autograd.Function``.
 """
 from __future__ import annotations
 

@@ -18,24 +18,32 @@ namespace moe {
 // Pairs of CTAs take tiles of 256 x 256, single ones 128 x 128 with twice the
 // bytes from L2 a flop, but four times as many tiles that end four times as
 // soon.  So pairs are for tiles that are many, filled well and long.  Single
-// and pair, us, on 40 experts: up at K = N = 2048, 102 and 96 with 192 rows an
-// expert, 512 and 389 with 1536; down at K = 512, N = 1024 (a contraction of
-// 512, 160 tiles), 27 and 31 with 384 rows, 41 and 41 with 768; down at K = 4096,
-// N = 512 (256, but 1280 tiles), 64 and 57 with 384 rows.  On 8 experts: down at
-// K = N = 2048, 25 and 26 with 256 rows; up at K = 4096, N = 1024 (32 tiles), 48
-// and 41 with 256.
+// and pair, us, each forced, on 40 experts: up at K = N = 2048, 122 and 102 with
+// 192 rows an expert, 638 and 476 with 1536; down at K = 512, N = 1024 (a
+// contraction of 512, 160 tiles), 24 and 25 with 384 rows, 38 and 35 with 768;
+// down at K = 4096, N = 512 (256, but 1280 tiles), 72 and 64 with 384 rows.  On 8
+// experts: down at K = N = 2048, 21 and 21 with 256 rows; up at K = 4096, N = 1024
+// (32 tiles), 41 and 35 with 256.  On 16: up at K = 1024, N = 2048, 32 and 29 with
+// 192.  The rule is a grid drawn through such points and misses some between
+// them: up at K = 960, N = 2048 on 16 experts, 31 and 27 with 192 rows, 45 and 42
+// with 384, runs on single CTAs until 410 rows.
 // Where a row's pitch is no multiple of 128 bytes, every 128 of an operand lie
 // in two lines of L2 and the bytes count for more: down at K = 1992, N = 1360,
-// 57 and 51 with 128 rows, 88 and 62 with 256.
+// 56 and 47 with 128 rows, 89 and 68 with 256; up at K = 1000, N = 720, 42 and 33
+// with 192; on 12 experts, down at K = 1000, N = 1360, 18 and 17 with 256; on 8, up
+// at K = 1000, N = 1008, 24 and 19 with 300.
 static bool pairs_for_rows(int64_t tiles, int64_t rows, int64_t contraction, bool lines) {
   if (tiles < 32 || rows < (lines ? 192 : 128)) return false;
   const int64_t least = !lines ? 80 : tiles >= 512 ? 96 : contraction >= 1000 ? 187 : 384;
   return rows * contraction >= least * 1024;
 }
-// Weight gradients, whose contraction is the rows, from 24 full tiles on: up_backward
-// at K = 4096, N = 1024 on 40 experts, 167 and 147 us with 64 rows, 218 and 175
-// with 192; down_backward at K = 512, N = 1024 on 8 experts, 20 and 15 with 64
-// (beside the rows' gradient there is room for few CTAs), 44 and 46 with 1536.
+// Weight gradients, whose contraction is the rows, from 24 tiles' elements on; whole
+// calls: up_backward at K = 4096, N = 1024 on 40 experts, 173 and 164 us with 64
+// rows, 230 and 213 with 192; down_backward at K = 512, N = 1024 on 8 experts, 15
+// and 15 with 64, 40 and 37 with 1536.  The elements stand for the tiles: a
+// gradient that fills its tiles badly takes pairs all the same and is up to an
+// eighth slower on them (up_backward at K = 4096, N = 16 on 64 experts of 256
+// rows, 96 and 107; down_backward at K = 264, N = 1040 on 24 of 128, 25 and 27).
 static bool pairs_for_weights(int64_t E, int64_t m, int64_t n) { return E * m * n >= 24 * 65536; }
 
 struct ExpertCall {

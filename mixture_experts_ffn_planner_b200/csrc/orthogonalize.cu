@@ -16,10 +16,12 @@
 // a X is taken from the pair: 2.0e-3, of which 1.7e-3 is the rounding of the
 // bf16 result.  From the fourth step on, when X is nearly orthogonal and B
 // nearly a multiple of I, the rounding of B's diagonal is what is left; it is
-// taken out of B into fp32 and joins a: 1.9e-3 to 2.3e-3 for matrices of
-// sides 32 to 1024, Gaussian, near-low-rank or with singular values over four
-// decades.  (Earlier it must not be: B's product with the strong directions
-// has to stay in one matrix product.)
+// taken out of B into fp32 and joins a: 1.7e-3 to 2.3e-3 for matrices of
+// sides 65 to 2048, Gaussian, of rank 1 to S/4 with noise or without, or with
+// singular values over two to eight decades.  (Earlier it must not be: B's
+// product with the strong directions has to stay in one matrix product.)
+// Where the values of a result are all alike (of the identity, or of a matrix
+// of ones) they are all rounded alike, by up to 2^-8, and 5.3e-3 was met.
 //
 // Three ways, by the sides:
 //   up to 64        fp32, without tensor cores (whose fp16 noise the steps may
@@ -43,8 +45,10 @@
 //
 // |G|_F is summed in 64 bits.  Every sum has a fixed order.  The launches of a
 // call are chained by programmatic dependent launch.  16 matrices of 2048 x
-// 2048 take 2.48 ms: a step 114 us for A, 112 for B (tensor pipe 72 % busy at
-// 1.58 GHz), 209 for the update, which moves 655 MB beside its product.
+// 2048 take 2.5 ms by themselves on a GPU that was idle, and 2.9 to 3.0 ms among
+// others of their kind under the power limit: a step 110 us for A, 109 for B
+// (tensor pipe 74 % busy at 1.58 GHz), 209 for the update, which moves 652 MB
+// beside its product.
 #include <algorithm>
 #include <cmath>
 
@@ -373,7 +377,7 @@ __device__ __forceinline__ void ns_outer32(const NsRow32* x, int n, int i0, int 
 
 // A cluster a matrix; `per` places of the longer side a CTA, lc >= per a
 // multiple of 64.  Bound by shared memory's reads for 4 x 4 sums a thread: 64 x
-// 64, 5 steps of three products of 64^3, takes 38 us (17 at 128 fmas a clock);
+// 64, 5 steps of three products of 64^3, takes 35 us (17 at 128 fmas a clock);
 // in 64 bits on one CTA it took 139.
 __global__ void __launch_bounds__(kNsThreads, 2)  // two an SM: 16 matrices of 64 x 2000 need 128 CTAs in clusters of 8
     ns_cluster_kernel(const NsSide n, int per, int lc, int steps, float a, float b, float c, double eps,

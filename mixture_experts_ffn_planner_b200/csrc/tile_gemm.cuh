@@ -12,10 +12,11 @@
 // cta_group::2 MMAs: each loads half of A's rows and half of B's, 32 KB a
 // chunk, and takes half of D's rows out of its own TMEM.  That is 128 flop a
 // byte from L2, where one CTA on a 128 x 256 tile has 85.  At 8192 tokens on 64
-// experts (K = N = 2048, cold L2) the gate/up product takes 434 us, one CTA
-// took 484; the tensor pipe is busy 84 % of the time at the 1.44 GHz that the
-// power limit leaves, of which an eighth goes to rows behind an expert's last
-// in 256-row tiles.  Otherwise one CTA works on 128 x 128: for experts with too
+// experts (K = N = 2048, cold L2) the gate/up product takes 434 us by itself on a
+// GPU that was idle, where one CTA took 484, and 540 to 550 among others of its
+// kind; the tensor pipe is busy 82 % of the time at the 1.44 GHz that the power
+// limit leaves, of which an eighth goes to rows behind an expert's last in
+// 256-row tiles.  Otherwise one CTA works on 128 x 128: for experts with too
 // few rows to fill 256, where the weights' bytes bound the call and 148 CTAs
 // stream more of them at once.
 //
